@@ -410,6 +410,110 @@ QE_API int qe_sekv_attend(const void* q, const void* K, const void* V, int B, in
                           int D, int dtype, float theta, void* state, size_t state_bytes,
                           float* out, qe_stream_t stream);
 
+/* Attention over whole prompts, packed one after another.
+ *   q [dev]: [T][Hq][D], k, v [dev]: [T][Hkv][D], fp16 or bf16 (dtype), each a view whose tokens
+ *     lie *_stride elements apart (so the three parts of a fused projection's rows will do): 16-byte
+ *     aligned, strides multiples of 8 and at least heads * D.
+ *   cu_seqlens [dev, int32]: [B + 1], sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1, with
+ *     0 <= cu_seqlens[b] <= cu_seqlens[b + 1] <= T. Empty sequences are allowed. Rows of the outputs
+ *     outside every sequence are left as they were, and such rows of the inputs may hold anything.
+ *   status [dev, int32]: [2] {code, detail}, zeroed by the caller once: the first device-side error
+ *     stays (QE_ERR_INVALID_ARG for bounds out of order, detail = the sequence, nothing is then
+ *     computed; QE_ERR_TIMEOUT if a bounded wait gave up).
+ * qe_prompt_attend: causal attention, query head h using kv head h / (Hq / Hkv), scale 1/sqrt(D):
+ *   out [dev]: [T][Hq][D] dtype, o_i = sum_{j <= i} p_ij v_j. The weights are rounded once to dtype for
+ *     the product; scores, maxima and sums are float32.
+ *   lse [dev, float, may be NULL]: [T][Hq] ln sum_{j <= i} exp(q_i . k_j / sqrt(D)).
+ *   The elements of a sequence's k and v must be finite (a row of v that is not reaches the outputs of
+ *   up to 127 positions before it).
+ * qe_prompt_mass: the weight each prompt token collects ("Resumo Técnico: QEvict", Pontuação
+ *   Cumulativa, over the prompt's own queries), from qe_prompt_attend's lse:
+ *   mass [dev, float]: [T][Hkv], mass_j = sum over the kv head's query heads and i >= j of
+ *     exp(q_i . k_j / sqrt(D) - lse_i).
+ * Errors (returned, nothing launched): QE_ERR_INVALID_ARG (null or misaligned pointer, a bad stride,
+ * B < 1, T < 0, Hq not a multiple of Hkv, bad dtype), QE_ERR_UNSUPPORTED_SHAPE (D not in {64, 128},
+ * Hq / Hkv > 8, T > 2^30). T == 0 does nothing. Asynchronous on `stream`; allocates nothing. */
+QE_API int qe_prompt_attend(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                            long long v_stride, const int32_t* cu_seqlens, int B, int T, int Hq, int Hkv, int D,
+                            int dtype, void* out, float* lse, int32_t* status, qe_stream_t stream);
+QE_API int qe_prompt_mass(const void* q, const void* k, long long q_stride, long long k_stride, const float* lse,
+                          const int32_t* cu_seqlens, int B, int T, int Hq, int Hkv, int D, int dtype, float* mass,
+                          int32_t* status, qe_stream_t stream);
+
+/* A cache held in 4 bits: K and V of every (sequence, kv head) unit u = b * Hkv + h in pages of 16
+ * entries, with the attention weight each entry has collected and its position in the sequence.
+ * Per entry and group of 32 consecutive elements: s = fp16(f32((max - min) / 15)), z = fp16(min),
+ * code = clamp(rint(f32(f32(x - z) / s)), 0, 15), 0 if s == 0, ties to even; the element stands for
+ * code * s + z. A page of 20 D bytes holds, with NG = D / 32:
+ *   K codes [16][4][NG] u32 (word (t, g), nibble j: element 32 g + 8 t + j),
+ *   V codes [16][8][NG] u16 (half (r, g), nibble j: element 32 g + 4 r + j),
+ *   K scales [16][NG] fp16, K zeros [16][NG] fp16,
+ *   V scales, then V zeros, [4][NG][2][2] fp16 at (t, g, hi, e) for entry 8 hi + 2 t + e.
+ * The caller owns every buffer. A physical page belongs to one unit (sharing one is allowed only
+ * while it is read and not weighed). Entries 0 .. lengths[u] - 1 of unit u are live, entry e in slot
+ * e % 16 of page page_table[u][e / 16]; slots behind them may hold anything.
+ *   status: zeroed by the caller once; the first device-side error stays: QE_ERR_INVALID_ARG (a
+ *     length out of range, detail = the unit, which counts as empty; bounds out of order, detail =
+ *     the sequence, nothing is done), QE_ERR_POOL_EXHAUSTED (an append that does not fit, detail =
+ *     the unit, which stays as it was), QE_ERR_DEVICE_FAULT (a page-table entry outside [0, n_pages),
+ *     detail = the unit; its entries count as absent), QE_ERR_TIMEOUT. The third word is the
+ *     library's own. One call at a time may use a cache. */
+typedef struct {
+  int B, Hkv, D;            /* sequences, kv heads, head dim (64 or 128)          */
+  int max_pages;            /* entries of a unit's page-table row                 */
+  int n_pages;              /* pages in the pool                                  */
+  void* pages;              /* [dev] [n_pages][20 * D] bytes, 16-byte aligned     */
+  int32_t* page_table;      /* [dev] [B * Hkv][max_pages]                         */
+  int32_t* lengths;         /* [dev] [B * Hkv] live entries of each unit          */
+  int32_t* seen;            /* [dev] [B] tokens appended to each sequence so far  */
+  float* mass;              /* [dev] [n_pages][16] weight collected by each entry */
+  int32_t* pos;             /* [dev] [n_pages][16] position of each entry         */
+  int32_t* status;          /* [dev] [4]                                          */
+} qe_int4_cache;
+
+/* qe_int4_append - quantise new tokens into the cache: a prompt, or one token a sequence.
+ *   k, v [dev]: [T][Hkv][D] dtype views with token strides as above (8-byte aligned, strides multiples
+ *     of 4); cu_seqlens [dev] [B + 1] as above. Token j of sequence b becomes entry lengths[u] + j of its
+ *     units, with position seen[b] + j and weight mass[t][h]; then lengths and seen move on by the
+ *     sequence's count. Elements must be finite and within fp16's range.
+ *   mass [dev, float, may be NULL = zeros]: [T][Hkv], e.g. from qe_prompt_mass.
+ * qe_int4_read - the values that entries stand for, rounded to float32 and then to dtype:
+ *   row t = cu_seqlens[b] + j of k_out, v_out [dev] [T][Hkv][D] receives entry first[u] + j (first [dev]
+ *   [B * Hkv], NULL = zeros); rows without such an entry are left as they were. */
+QE_API int qe_int4_append(const qe_int4_cache* cache, const void* k, const void* v, long long k_stride,
+                          long long v_stride, const int32_t* cu_seqlens, int T, int dtype, const float* mass,
+                          qe_stream_t stream);
+QE_API int qe_int4_read(const qe_int4_cache* cache, const int32_t* cu_seqlens, int T, const int32_t* first, int dtype,
+                        void* k_out, void* v_out, qe_stream_t stream);
+
+/* qe_int4_attend - one decode step's attention over the cache:
+ *   out_h = sum_i p_hi v_i, p_h = softmax_i(q_h . k_i / sqrt(D)) over the unit's live entries, k and v
+ *   being the values they stand for; 0 for a unit without entries. With accumulate != 0 every entry's
+ *   weight grows: mass_i += sum over the unit's query heads of p_hi.
+ *   q [dev]: [B][Hq][D] dtype, rows q_stride elements apart (16-byte aligned, a multiple of 8).
+ *   out [dev]: [B][Hq][D] dtype. The weights are rounded to fp16 for the product with v.
+ *   scratch [dev]: qe_int4_scratch_bytes(B, Hq, Hkv, D, max_pages) bytes, 256-byte aligned, not shared
+ *     by concurrent calls.
+ * Further errors: QE_ERR_UNSUPPORTED_SHAPE (Hq / Hkv > 8, B * Hkv > 65535), QE_ERR_WORKSPACE. */
+QE_API size_t qe_int4_scratch_bytes(int B, int Hq, int Hkv, int D, int max_pages);
+QE_API int qe_int4_attend(const qe_int4_cache* cache, const void* q, long long q_stride, int Hq, int dtype,
+                          int accumulate, void* out, void* scratch, size_t scratch_bytes, qe_stream_t stream);
+
+/* qe_int4_evict - copy what is kept of a cache into another one ("Resumo Técnico: QEvict", Pontuação
+ * Cumulativa, entry by entry): of each unit of src the entries of position >= seen[b] - recent, and
+ * of the others those of highest weight, `budget` in all (every entry when there are no more); among
+ * equals the lower entry. A NaN weight is below every other. Their records move byte for byte, with
+ * weight and position, to entries 0, 1, ... of dst in their order; dst's lengths and seen are
+ * written, src stays as it was, slots of dst behind the last entry stay as they were.
+ *   src, dst: equal B, Hkv and D; no buffer of dst but its page_table and status may be one of src's;
+ *     dst holds at least `budget` entries a unit.
+ * All qe_int4_* errors (returned, nothing launched): QE_ERR_INVALID_ARG (null or misaligned pointer, bad
+ * sizes or strides, budget < 1 or above dst's capacity, recent < 0, shared buffers),
+ * QE_ERR_UNSUPPORTED_SHAPE (D not in {64, 128}, B * Hkv * max_pages * 16 >= 2^31). T == 0 does nothing.
+ * Asynchronous on `stream`; allocates nothing. */
+QE_API int qe_int4_evict(const qe_int4_cache* src, const qe_int4_cache* dst, int budget, int recent,
+                         qe_stream_t stream);
+
 /* qe_state_bytes / qe_state_export / qe_state_import - checkpoint and restore of one context:
  * the persistent state the pages describe ("Resumo Técnico: QEvict", Hierarquia Recuperável:
  * the write-once INT2 ledger; Pontuação Cumulativa: the cumulative window scores), together with

@@ -36,6 +36,11 @@ class QeDiagStats(C.Structure):
                                             "windows_reentered")] + [("churn", C.c_double), ("lir", C.c_double)]
 
 
+class QeInt4Cache(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("B", "Hkv", "D", "max_pages", "n_pages")] + \
+               [(n, C.c_void_p) for n in ("pages", "page_table", "lengths", "seen", "mass", "pos", "status")]
+
+
 class QeLayout(C.Structure):
     _fields_ = [(n, C.c_size_t) for n in ("total", "pages", "page_free", "win_pages", "win_tier",
                                            "win_slot", "slots", "slot_free", "mass", "pert", "norms",
@@ -87,6 +92,13 @@ def lib():
             "qe_state_bytes": (sz, [vp]),
             "qe_state_export": (i, [vp, vp, sz, vp]),
             "qe_state_import": (i, [vp, vp, sz, vp]),
+            "qe_prompt_attend": (i, [vp, vp, vp, ll, ll, ll, vp, i, i, i, i, i, i, vp, vp, vp, vp]),
+            "qe_prompt_mass": (i, [vp, vp, ll, ll, vp, vp, i, i, i, i, i, i, vp, vp, vp]),
+            "qe_int4_append": (i, [C.POINTER(QeInt4Cache), vp, vp, ll, ll, vp, i, i, vp, vp]),
+            "qe_int4_read": (i, [C.POINTER(QeInt4Cache), vp, i, vp, i, vp, vp, vp]),
+            "qe_int4_scratch_bytes": (sz, [i, i, i, i, i]),
+            "qe_int4_attend": (i, [C.POINTER(QeInt4Cache), vp, ll, i, i, i, vp, vp, sz, vp]),
+            "qe_int4_evict": (i, [C.POINTER(QeInt4Cache), C.POINTER(QeInt4Cache), i, i, vp]),
             "qe_diag_summary": (i, [vp, i, C.POINTER(QeDiagStats), vp]),
             "qe_status": (i, [vp, C.POINTER(C.c_int)]),
             "qe_step_index": (i, [vp]),
@@ -580,3 +592,180 @@ def sekv_views(state: torch.Tensor, B: int, Hq: int, Hkv: int, n: int, D: int) -
             "vbar": view(off[5], B * Hkv * cap * D, torch.float32, (B, Hkv, cap, D)),
             "expanded": view(off[6], B * Hkv * cap, torch.uint8, (B, Hkv, cap)),
             "cap": cap}
+
+
+# ---------------------------------------------------------------------------------
+# prompts and the 4-bit cache
+# ---------------------------------------------------------------------------------
+
+
+def _tokens(t: torch.Tensor, name: str, heads: int, D: int, dtype, T=None) -> int:
+    """Check a [T][heads][D] CUDA view whose tokens may be strided; its token stride in elements."""
+    if not t.is_cuda or t.dim() != 3 or t.dtype != dtype:
+        raise ValueError(f"{name} must be a 3-D {dtype} CUDA tensor")
+    if t.shape[1] != heads or t.shape[2] != D or (T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} must have shape {(T, heads, D)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"the heads and elements of {name} must be contiguous within a token")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def _same_device(dev, *named):
+    for t, name in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, out=None, lse=None,
+                  status=None, stream=None):
+    """Causal attention over packed prompts (qe_prompt_attend).
+
+    q [T][Hq][D], k and v [T][Hkv][D] (fp16 or bf16; tokens may be strided, as in the parts of a
+    fused projection), cu_seqlens [B + 1] int32 on the device. Returns (out [T][Hq][D], lse [T][Hq]
+    float32, status [2] int32, its device status word; pass one zeroed once to reuse it). Rows of
+    out and lse outside every sequence are left as they were.
+    """
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    dev = q.device
+    qs = _tokens(q, "q", Hq, D, q.dtype)
+    ks = _tokens(k, "k", Hkv, D, q.dtype, T)
+    vs = _tokens(v, "v", Hkv, D, q.dtype, T)
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    with torch.cuda.device(dev):
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+        status = torch.zeros(2, dtype=torch.int32, device=dev) if status is None else status
+        _need(out, "out", q.dtype, (T, Hq, D))
+        _need(lse, "lse", torch.float32, (T, Hq))
+        _need(status, "status", torch.int32)
+        _same_device(dev, (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens"), (out, "out"), (lse, "lse"), (status, "status"))
+        _check(lib().qe_prompt_attend(_ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(cu_seqlens), cu_seqlens.numel() - 1,
+                                      T, Hq, Hkv, D, dtype_code(q.dtype), _ptr(out), _ptr(lse), _ptr(status),
+                                      _stream(stream)), "qe_prompt_attend")
+    return out, lse, status
+
+
+def prompt_mass(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_seqlens: torch.Tensor, mass=None, status=None,
+                stream=None):
+    """The attention weight each prompt token collects (qe_prompt_mass), from prompt_attend's inputs
+    and lse. Returns (mass [T][Hkv] float32, status)."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    dev = q.device
+    qs = _tokens(q, "q", Hq, D, q.dtype)
+    ks = _tokens(k, "k", Hkv, D, q.dtype, T)
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    _need(lse, "lse", torch.float32, (T, Hq))
+    with torch.cuda.device(dev):
+        mass = torch.empty((T, Hkv), dtype=torch.float32, device=dev) if mass is None else mass
+        status = torch.zeros(2, dtype=torch.int32, device=dev) if status is None else status
+        _need(mass, "mass", torch.float32, (T, Hkv))
+        _need(status, "status", torch.int32)
+        _same_device(dev, (k, "k"), (lse, "lse"), (cu_seqlens, "cu_seqlens"), (mass, "mass"), (status, "status"))
+        _check(lib().qe_prompt_mass(_ptr(q), _ptr(k), qs, ks, _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T,
+                                    Hq, Hkv, D, dtype_code(q.dtype), _ptr(mass), _ptr(status), _stream(stream)),
+               "qe_prompt_mass")
+    return mass, status
+
+
+class Int4Cache:
+    """A cache held in 4 bits (qe_int4_*): K and V of each (sequence, kv head) unit in pages of 16
+    entries, the attention weight every entry has collected, and its position.
+
+    Owns its buffers: pages [n_pages][20 D] uint8, page_table [U][max_pages] int32 (consecutive pages
+    unless the caller fills it otherwise), counts [U + B] int32 (lengths [U], then the tokens seen by
+    each sequence [B]), mass and pos [n_pages][16], and the status word (see status_word). One
+    step of use: append, attend, and every so often evict into another cache.
+    """
+
+    def __init__(self, B: int, Hkv: int, D: int, capacity: int, device="cuda"):
+        if B < 1 or Hkv < 1 or capacity < 1:
+            raise ValueError("B, Hkv and capacity must be positive")
+        self.B, self.Hkv, self.D, self.units = B, Hkv, D, B * Hkv
+        self.max_pages = -(-capacity // 16)
+        n = self.units * self.max_pages
+        self.pages = torch.zeros((n, 20 * D), dtype=torch.uint8, device=device)
+        self.device = self.pages.device
+        self.page_table = torch.arange(n, dtype=torch.int32, device=device).view(self.units, self.max_pages)
+        self.counts = torch.zeros(self.units + B, dtype=torch.int32, device=device)
+        self.lengths, self.seen = self.counts[:self.units], self.counts[self.units:]
+        self.mass = torch.zeros((n, 16), dtype=torch.float32, device=device)
+        self.pos = torch.zeros((n, 16), dtype=torch.int32, device=device)
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self._scratch = {}
+        self._c = QeInt4Cache(B, Hkv, D, self.max_pages, n, *(t.data_ptr() for t in (
+            self.pages, self.page_table, self.lengths, self.seen, self.mass, self.pos, self.status)))
+
+    def status_word(self):
+        """(code, detail) of the device status word; synchronises."""
+        w = self.status.cpu()
+        return int(w[0]), int(w[1])
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, mass=None, stream=None):
+        """Quantise new tokens k, v [T][Hkv][D] (tokens may be strided), sequence b's in rows
+        cu_seqlens[b] .. cu_seqlens[b + 1] - 1, with the weights mass [T][Hkv] float32 (None: zeros)."""
+        T = k.shape[0]
+        ks = _tokens(k, "k", self.Hkv, self.D, k.dtype)
+        vs = _tokens(v, "v", self.Hkv, self.D, k.dtype, T)
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,))
+        if mass is not None:
+            _need(mass, "mass", torch.float32, (T, self.Hkv))
+        _same_device(self.device, (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens"), (mass, "mass"))
+        with torch.cuda.device(self.device):
+            _check(lib().qe_int4_append(C.byref(self._c), _ptr(k), _ptr(v), ks, vs, _ptr(cu_seqlens), T,
+                                        dtype_code(k.dtype), None if mass is None else _ptr(mass), _stream(stream)),
+                   "qe_int4_append")
+
+    def read(self, cu_seqlens: torch.Tensor, T: int, first=None, dtype=torch.bfloat16, k_out=None, v_out=None,
+             stream=None):
+        """Values of entries first[u] + j of the units of sequence b in rows cu_seqlens[b] + j of
+        (k_out, v_out) [T][Hkv][D]; rows without such an entry are left as they were."""
+        shape = (T, self.Hkv, self.D)
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,))
+        if first is not None:
+            _need(first, "first", torch.int32, (self.units,))
+        with torch.cuda.device(self.device):
+            k_out = torch.empty(shape, dtype=dtype, device=self.device) if k_out is None else k_out
+            v_out = torch.empty(shape, dtype=dtype, device=self.device) if v_out is None else v_out
+            _need(k_out, "k_out", dtype, shape)
+            _need(v_out, "v_out", dtype, shape)
+            _same_device(self.device, (cu_seqlens, "cu_seqlens"), (first, "first"), (k_out, "k_out"), (v_out, "v_out"))
+            _check(lib().qe_int4_read(C.byref(self._c), _ptr(cu_seqlens), T, None if first is None else _ptr(first),
+                                      dtype_code(dtype), _ptr(k_out), _ptr(v_out), _stream(stream)), "qe_int4_read")
+        return k_out, v_out
+
+    def scratch(self, Hq: int) -> torch.Tensor:
+        """The scratch buffer that attend uses for this many query heads (made on first use)."""
+        s = self._scratch.get(Hq)
+        if s is None:
+            n = int(lib().qe_int4_scratch_bytes(self.B, Hq, self.Hkv, self.D, self.max_pages))
+            if n == 0:
+                raise ValueError("unsupported shape")
+            s = self._scratch[Hq] = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return s
+
+    def attend(self, q: torch.Tensor, out=None, accumulate: bool = True, scratch=None, stream=None) -> torch.Tensor:
+        """One step's attention: q [B][Hq][D] (rows may be strided) over every live entry; returns out
+        [B][Hq][D] in q's dtype. With accumulate the entries' weights grow by what they receive."""
+        B, Hq, D = q.shape
+        if B != self.B or D != self.D:
+            raise ValueError(f"q must be [{self.B}][Hq][{self.D}], got {tuple(q.shape)}")
+        qs = _tokens(q, "q", Hq, D, q.dtype)
+        with torch.cuda.device(self.device):
+            out = torch.empty((B, Hq, D), dtype=q.dtype, device=self.device) if out is None else out
+            _need(out, "out", q.dtype, (B, Hq, D))
+            scratch = self.scratch(Hq) if scratch is None else scratch
+            _same_device(self.device, (q, "q"), (out, "out"), (scratch, "scratch"))
+            _check(lib().qe_int4_attend(C.byref(self._c), _ptr(q), qs, Hq, dtype_code(q.dtype), int(accumulate),
+                                        _ptr(out), _ptr(scratch), scratch.numel(), _stream(stream)), "qe_int4_attend")
+        return out
+
+    def evict(self, into: "Int4Cache", budget: int, recent: int, stream=None) -> "Int4Cache":
+        """Copy each unit's `recent` newest entries and the heaviest others, `budget` in all, into
+        another cache (its lengths, weights and positions are written; this one stays as it was)."""
+        _same_device(self.device, (into.pages, "into"))
+        with torch.cuda.device(self.device):
+            _check(lib().qe_int4_evict(C.byref(self._c), C.byref(into._c), budget, recent, _stream(stream)),
+                   "qe_int4_evict")
+        return into

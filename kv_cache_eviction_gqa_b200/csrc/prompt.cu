@@ -1,0 +1,707 @@
+// Attention over whole prompts, packed one after another, and the attention weight that each
+// prompt token collects (the cumulative score of "Resumo Técnico: QEvict", Pontuação Cumulativa,
+// taken over the prompt's own queries).
+//
+//   qe_prompt_attend: per query head h of kv head g and position i of a sequence,
+//     o_i = sum_{j <= i} p_ij v_j,  p_ij = exp(q_i.k_j / sqrt(D) - lse_i),
+//     lse_i = ln sum_{j <= i} exp(q_i.k_j / sqrt(D)).
+//   qe_prompt_mass:   mass_j = sum_{h in g} sum_{i >= j} p_ij, from q, k and the lse above.
+//
+// Both walk tiles of 128 packed query rows: the G query heads of a kv head share its keys, so row
+// r of a tile is position r / G, head r % G, PT = floor(128 / G) positions to a tile. One 3-D TMA
+// box (64 elements, G heads, PT tokens) brings such a tile in, whatever the token stride.
+#include <math.h>
+
+#include "tc_common.cuh"
+
+namespace {
+
+using namespace tc;
+
+constexpr int kTileM = 128;             // packed query rows, keys, and accumulator columns of a tile
+constexpr int kBoxBytes = 128 * 128;    // 128 rows x 64 16-bit elements
+constexpr int kTmemAll = 512;
+constexpr int kRoleWarps = 8;           // two groups of four: one TMEM lane a thread, a tile a group
+constexpr int kPromptThreads = (kRoleWarps + 2) * 32;
+
+struct PromptArgs {
+  const int32_t* cu;      // [B + 1]
+  int B, T, G, Hq, Hkv, PT;
+  float c;                // log2(e) / sqrt(D)
+  void* out;              // [T][Hq][D]
+  float* lse;             // [T][Hq]
+  const float* lse_in;
+  float* mass;            // [T][Hkv]
+  int32_t* status;
+};
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A operand in TMEM (16-bit pairs, one row a lane), B in shared memory
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#define QE_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), \
+                    "=r"(v[o + 6]), "=r"(v[o + 7])
+#define QE_W8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), \
+                    "r"(v[o + 6]), "r"(v[o + 7])
+// 32 consecutive columns of this thread's lane; complete after tmem_wait_ld
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : QE_R8(v, 0), QE_R8(v, 8), QE_R8(v, 16), QE_R8(v, 24)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::QE_W8(v, 0),
+      QE_W8(v, 8), QE_W8(v, 16), QE_W8(v, 24), "r"(taddr)
+      : "memory");
+}
+#undef QE_R8
+#undef QE_W8
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------------------
+// which tile a CTA takes
+// ---------------------------------------------------------------------------------------
+
+struct TileRef {
+  int start, len, tile;   // first row of the sequence, its tokens, tile index; len 0: nothing to do
+};
+
+// Tiles of P positions of all sequences in the order of falling work, work w being the number of
+// the tiles of the sequence on one side of it (this one included): F(w) = sum_b max(0, tiles_b -
+// w + 1) tiles have work >= w, so rank r has the largest w with F(w) > r, and is the (r - F(w +
+// 1))-th sequence of at least w tiles. One warp finds it without a list: the last CTAs to start
+// are the shortest ones. Bad bounds (not in 0 <= cu[b] <= cu[b + 1] <= T) are recorded, and the
+// call does nothing.
+__device__ TileRef find_tile(const PromptArgs& a, int P, int rank, bool from_end) {
+  const int lane = threadIdx.x & 31;
+  int most = 0, bad = 0x7fffffff;
+  for (int b = lane; b < a.B; b += 32) {
+    const int s = a.cu[b], e = a.cu[b + 1];
+    if (s < 0 || e < s || e > a.T) bad = min(bad, b);
+    most = max(most, (e - s + P - 1) / P);
+  }
+  bad = __reduce_min_sync(0xffffffffu, bad);
+  most = __reduce_max_sync(0xffffffffu, most);
+  TileRef t{0, 0, 0};
+  if (bad != 0x7fffffff) {
+    if (lane == 0) qe_record_error(a.status, QE_ERR_INVALID_ARG, bad);
+    return t;
+  }
+  auto at_least = [&](int w) {
+    int f = 0;
+    for (int b = lane; b < a.B; b += 32) f += max(0, (a.cu[b + 1] - a.cu[b] + P - 1) / P - w + 1);
+    return __reduce_add_sync(0xffffffffu, f);
+  };
+  if (most == 0 || at_least(1) <= rank) return t;
+  int lo = 1, hi = most;                 // F(lo) > rank
+  while (lo < hi) {
+    const int w = (lo + hi + 1) >> 1;
+    if (at_least(w) > rank) lo = w; else hi = w - 1;
+  }
+  int r = rank - (lo < most ? at_least(lo + 1) : 0);
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int n = b < a.B ? a.cu[b + 1] - a.cu[b] : 0, tiles = (n + P - 1) / P;
+    const uint32_t has = __ballot_sync(0xffffffffu, tiles >= lo);
+    if (r < __popc(has)) {
+      const bool mine = (has >> lane & 1) && __popc(has & ((1u << lane) - 1u)) == r;
+      const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+      t.start = __shfl_sync(0xffffffffu, b < a.B ? a.cu[b] : 0, src);
+      t.len = __shfl_sync(0xffffffffu, n, src);
+      t.tile = from_end ? __shfl_sync(0xffffffffu, tiles, src) - lo : lo - 1;
+      return t;
+    }
+    r -= __popc(has);
+  }
+  return t;
+}
+
+// ---------------------------------------------------------------------------------------
+// prompt attention
+// ---------------------------------------------------------------------------------------
+
+// A CTA owns two tiles of one kv head, 2 PT consecutive positions, and streams the keys and values
+// they see through a ring of 128-row tiles. Warp roles:
+//   warps 0-3, 4-7  softmax of tile 0, tile 1: a thread owns a row (a TMEM lane). It reads the
+//                   row's 128 scores, keeps the running maximum m and sum l of exp2(c s - c m),
+//                   and writes the weights as 16-bit pairs over the scores. m only follows the true
+//                   maximum when that has risen by 2^8; then the row of O is rescaled in TMEM.
+//   warp 8          TMA: both query tiles, then K_0 V_0 K_1 V_1 ...
+//   warp 9          tcgen05.mma: S_t = Q_t K^T, O_t += P_t V, the tiles in turn, so one tile's
+//                   softmax runs under the other's products.
+// TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each; P_t lies over the first half of S_t (the products
+// that read it are issued before those that write the next scores).
+template <int D>
+struct AttendSmem {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * kBoxBytes;
+  static constexpr int NS = D == 128 ? 5 : 6;     // ring stages
+  static constexpr int BYTES = 1024 + (2 + NS) * TILE + 256;
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, PromptArgs a) {
+  using S = AttendSmem<D>;
+  constexpr uint32_t ID_QK = idesc_f16(BF16, false, kTileM, kTileM);
+  constexpr uint32_t ID_PV = idesc_f16(BF16, true, kTileM, D);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * S::TILE;
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(sKV + S::NS * S::TILE);   // [2]
+  uint64_t* full = qfull + 2;                                             // [NS]
+  uint64_t* empty = full + S::NS;                                         // [NS]
+  uint64_t* sfull = empty + S::NS;                                        // [2] scores in TMEM
+  uint64_t* pfull = sfull + 2;                                            // [2] weights in TMEM
+  uint64_t* odone = pfull + 2;                                            // [2] P V added
+  uint64_t* vclean = odone + 2;                                           // foreign rows of the last V cleared
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vclean + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* sTile = reinterpret_cast<int*>(tmem_slot + 2);                     // [3]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.x % a.Hkv;
+  if (warp == 0) {
+    const TileRef t = find_tile(a, 2 * a.PT, blockIdx.x / a.Hkv, false);
+    if (lane == 0) sTile[0] = t.start, sTile[1] = t.len, sTile[2] = t.tile;
+  }
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 1);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+      mbar_init(&odone[i], 1);
+    }
+    for (int s = 0; s < S::NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(vclean, 4);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, kTmemAll);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int start = sTile[0], len = sTile[1], pos0 = sTile[2] * 2 * a.PT;
+  // key tiles that each query tile sees: up to its last position inside the sequence
+  int nt[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int end = min(len, pos0 + (t + 1) * a.PT);
+    nt[t] = pos0 + t * a.PT < len ? (end + kTileM - 1) / kTileM : 0;
+  }
+  const int N = max(nt[0], nt[1]);
+  // the last key tile holds rows behind the sequence: their weights are 0, but 0 x NaN is not
+  const bool dirty = N * kTileM > len;
+  const int clears = nt[1] == N ? 1 : 0;   // the group that sees the last tile clears those rows
+
+  if (len > 0 && warp == 8) {
+    if (lane == 0) {
+      for (int t = 0; t < 2; ++t) {
+        if (nt[t] == 0) continue;
+        mbar_arrive_expect_tx(&qfull[t], S::KB * a.G * a.PT * 128);
+        for (int kb = 0; kb < S::KB; ++kb)
+          tma_load_3d(sQ + t * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + pos0 + t * a.PT, &qfull[t]);
+      }
+      for (int i = 0; i < 2 * N; ++i) {
+        const int s = i % S::NS;
+        if (!wait_or_abort(&empty[s], ((i / S::NS) & 1) ^ 1, abort_flag, a.status, 5001)) break;
+        mbar_arrive_expect_tx(&full[s], S::TILE);
+        const CUtensorMap* tm = (i & 1) ? &tmV : &tmK;
+        for (int kb = 0; kb < S::KB; ++kb)
+          tma_load_3d(sKV + s * S::TILE + kb * kBoxBytes, tm, kb * 64, kvh, start + (i >> 1) * kTileM, &full[s]);
+      }
+    }
+  } else if (len > 0 && warp == 9) {
+    if (lane == 0) {
+      auto wait_full = [&](int i) {
+        return wait_or_abort(&full[i % S::NS], (i / S::NS) & 1, abort_flag, a.status, 5002);
+      };
+      auto qk = [&](int t, int i) {       // S_t = Q_t K_i^T
+        const uint8_t* sK = sKV + ((2 * i) % S::NS) * S::TILE;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * kBoxBytes + (k % 4) * 32;
+          mma_f16(tmem + t * kTileM, sdesc(smem_u32(sQ + t * S::TILE + off), 16, 1024),
+                  sdesc(smem_u32(sK + off), 16, 1024), ID_QK, k > 0 ? 1u : 0u);
+        }
+        mma_commit(&sfull[t]);
+      };
+      bool ok = wait_full(0);
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (nt[t] == 0) continue;
+        ok = wait_or_abort(&qfull[t], 0, abort_flag, a.status, 5003);
+        tc_fence_after();
+        if (ok) qk(t, 0);
+      }
+      if (ok && S::NS < 2 * N) mma_commit(&empty[0]);
+      for (int i = 0; i < N && ok; ++i) {
+        const int sv = (2 * i + 1) % S::NS;
+        ok = wait_full(2 * i + 1);
+        if (ok && i == N - 1 && dirty) ok = wait_or_abort(vclean, 0, abort_flag, a.status, 5004);
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (i < nt[t]) {
+            ok = wait_or_abort(&pfull[t], i & 1, abort_flag, a.status, 5005);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kTileM / 16; ++k)
+              mma_f16_ts(tmem + 2 * kTileM + t * kTileM, tmem + t * kTileM + k * 8,
+                         sdesc(smem_u32(sKV + sv * S::TILE + k * 16 * 128), kBoxBytes, 1024), ID_PV,
+                         i > 0 || k > 0 ? 1u : 0u);
+            mma_commit(&odone[t]);
+          }
+          if (t == 1 && 2 * i + 1 + S::NS < 2 * N) mma_commit(&empty[sv]);
+          if (i + 1 < N) {
+            if (t == 0) ok = wait_full(2 * i + 2);
+            if (ok && i + 1 < nt[t]) qk(t, i + 1);
+            if (t == 1 && 2 * i + 2 + S::NS < 2 * N) mma_commit(&empty[(2 * i + 2) % S::NS]);
+          }
+        }
+      }
+    }
+  } else if (len > 0) {
+    // ---- softmax ----
+    const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t tS = lane_addr + t * kTileM, tO = lane_addr + 2 * kTileM + t * kTileM;
+    const int pos = pos0 + t * a.PT + r / a.G;
+    const int n = nt[t];
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    auto clear_foreign = [&]() {        // rows >= len of the last V tile
+      const int i = 2 * (N - 1) + 1;
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&full[i % S::NS], (i / S::NS) & 1, abort_flag, a.status, 5006));
+      if (!ok) return;
+      uint8_t* sV = sKV + (i % S::NS) * S::TILE;
+      const int row0 = len - (N - 1) * kTileM;
+      for (int x = row0 * 8 + r; x < kTileM * 8; x += kTileM)
+        for (int kb = 0; kb < S::KB; ++kb)
+          *reinterpret_cast<uint4*>(sV + kb * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vclean);
+    };
+    for (int i = 0; i < n && ok; ++i) {
+      ok = __all_sync(0xffffffffu, wait_or_abort(&sfull[t], i & 1, abort_flag, a.status, 5007));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v[kTileM];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tmem_ld_x32(tS + 32 * j, v + 32 * j);
+      tmem_wait_ld();
+      const int lim = pos - i * kTileM;   // columns 0..lim are seen
+      if (i * kTileM + kTileM - 1 > pos0 + t * a.PT) {
+#pragma unroll
+        for (int j = 0; j < kTileM; ++j)
+          if (j > lim) v[j] = 0xff800000u;
+      }
+      float mx = m;
+#pragma unroll
+      for (int j = 0; j < kTileM; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
+      const bool up = (mx - m) * a.c > 8.f;          // true on the first tile (m = -inf)
+      const float mo = m;
+      if (up) m = mx;
+      if (i > 0 && __any_sync(0xffffffffu, up)) {
+        const float f = up ? ex2f((mo - m) * a.c) : 1.f;
+        l *= f;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&odone[t], (i - 1) & 1, abort_flag, a.status, 5008));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t o[32];
+          tmem_ld_x32(tO + 32 * j, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+          tmem_st_x32(tO + 32 * j, o);
+        }
+      }
+      const float mc = m * a.c;
+      float2 sum = make_float2(0.f, 0.f);
+      // the weights are rounded once, to the type of V, for the product; their sum is not
+#pragma unroll
+      for (int j = 0; j < kTileM; j += 2) {
+        const float x = ex2f(fmaf(__uint_as_float(v[j]), a.c, -mc));
+        const float y = ex2f(fmaf(__uint_as_float(v[j + 1]), a.c, -mc));
+        sum = __fadd2_rn(sum, make_float2(x, y));
+        if (BF16)
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[j / 2]) : "f"(y), "f"(x));
+        else
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[j / 2]) : "f"(y), "f"(x));
+      }
+      l += sum.x + sum.y;
+      tmem_st_x32(tS, v);
+      tmem_st_x32(tS + 32, v + 32);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[t]);
+      if (i == N - 1 && dirty && t == clears) clear_foreign();
+    }
+    if (n > 0 && ok)
+      ok = __all_sync(0xffffffffu, wait_or_abort(&odone[t], (n - 1) & 1, abort_flag, a.status, 5009));
+    if (n > 0 && ok) {
+      tc_fence_after();
+      const float inv = 1.f / l;
+      const bool mine = r < a.G * a.PT && pos < len;
+      const size_t row = (size_t)(start + pos) * a.Hq + kvh * a.G + r % a.G;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * 2);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        uint32_t o[32];
+        tmem_ld_x32(tO + 32 * j, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float lo = __uint_as_float(o[x]) * inv, hi = __uint_as_float(o[x + 1]) * inv;
+          if (BF16)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
+          else
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
+        }
+        if (mine) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            dst[j * 4 + x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
+      }
+      if (mine && a.lse) a.lse[row] = (m * a.c + log2f(l)) * 0.693147180559945309f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// accumulated weight of the prompt's tokens
+// ---------------------------------------------------------------------------------------
+
+// A CTA owns 256 keys of one kv head, two tiles of 128, and streams the packed query tiles that see
+// them. The scores are taken with the keys as rows, S = K Q^T, so a thread owns a key and its sum
+// over queries never leaves its registers: mass = sum_r exp2(c s_r - log2(e) lse_r). Warp roles as
+// above; each group's scores go through two TMEM buffers (2 tiles x 2 x 128 columns), so the
+// products run ahead of the exponentials that bound this kernel.
+template <int D>
+struct MassSmem {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * kBoxBytes;
+  static constexpr int NS = 3;
+  static constexpr int NB = 4;                       // lse rows in flight (a power of two)
+  static constexpr int BYTES = 1024 + (2 + NS) * TILE + NB * kTileM * 4 + 256;
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, PromptArgs a) {
+  using S = MassSmem<D>;
+  constexpr uint32_t ID = idesc_f16(BF16, false, kTileM, kTileM);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sK = smem;
+  uint8_t* sQ = smem + 2 * S::TILE;
+  float* sL = reinterpret_cast<float*>(sQ + S::NS * S::TILE);             // [2][2][128]: per group, double
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(sL + S::NB * kTileM);
+  uint64_t* full = kfull + 1;                                             // [NS]
+  uint64_t* empty = full + S::NS;                                         // [NS]
+  uint64_t* sfull = empty + S::NS;                                        // [2 tiles][2]
+  uint64_t* sfree = sfull + 4;                                            // [2 tiles][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sfree + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* sTile = reinterpret_cast<int*>(tmem_slot + 2);                     // [3]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.x % a.Hkv;
+  if (warp == 0) {
+    const TileRef t = find_tile(a, 2 * kTileM, blockIdx.x / a.Hkv, true);
+    if (lane == 0) sTile[0] = t.start, sTile[1] = t.len, sTile[2] = t.tile;
+  }
+  if (threadIdx.x == 32) {
+    mbar_init(kfull, 1);
+    for (int s = 0; s < S::NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&sfull[b], 1);
+      mbar_init(&sfree[b], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, kTmemAll);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int start = sTile[0], len = sTile[1], key0 = sTile[2] * 2 * kTileM;
+  const int two = key0 + kTileM < len ? 2 : 1;           // key tiles inside the sequence
+  const int qt0 = key0 / a.PT, qt1 = (len + a.PT - 1) / a.PT;   // query tiles that see them
+  const int N = len > 0 ? qt1 - qt0 : 0;
+
+  if (N > 0 && warp == 8) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kfull, two * S::TILE);
+      for (int t = 0; t < two; ++t)
+        for (int kb = 0; kb < S::KB; ++kb)
+          tma_load_3d(sK + t * S::TILE + kb * kBoxBytes, &tmK, kb * 64, kvh, start + key0 + t * kTileM, kfull);
+      for (int i = 0; i < N; ++i) {
+        const int s = i % S::NS;
+        if (!wait_or_abort(&empty[s], ((i / S::NS) & 1) ^ 1, abort_flag, a.status, 5101)) break;
+        mbar_arrive_expect_tx(&full[s], S::KB * a.G * a.PT * 128);
+        for (int kb = 0; kb < S::KB; ++kb)
+          tma_load_3d(sQ + s * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + (qt0 + i) * a.PT, &full[s]);
+      }
+    }
+  } else if (N > 0 && warp == 9) {
+    if (lane == 0 && wait_or_abort(kfull, 0, abort_flag, a.status, 5102)) {
+      bool ok = true;
+      for (int i = 0; i < N && ok; ++i) {
+        const int s = i % S::NS, b = i & 1;
+        ok = wait_or_abort(&full[s], (i / S::NS) & 1, abort_flag, a.status, 5103);
+        for (int t = 0; t < two && ok; ++t) {
+          ok = wait_or_abort(&sfree[2 * t + b], ((i >> 1) & 1) ^ 1, abort_flag, a.status, 5104);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * kBoxBytes + (k % 4) * 32;
+            mma_f16(tmem + (2 * t + b) * kTileM, sdesc(smem_u32(sK + t * S::TILE + off), 16, 1024),
+                    sdesc(smem_u32(sQ + s * S::TILE + off), 16, 1024), ID, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&sfull[2 * t + b]);
+        }
+        if (i + S::NS < N) mma_commit(&empty[s]);
+      }
+    }
+  } else if (N > 0) {
+    const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
+    const int key = key0 + t * kTileM + r;
+    const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+    const int gr = threadIdx.x & 127;                    // the query row whose lse this thread fetches
+    const int gp = gr / a.G, gh = gr % a.G;
+    float* gL = sL + t * 2 * kTileM;
+    const int rows = a.G * a.PT;
+    auto fetch = [&](int i) -> float {
+      const int p = (qt0 + i) * a.PT + gp;
+      return gr < rows && p < len
+                 ? a.lse_in[(size_t)(start + p) * a.Hq + kvh * a.G + gh] * 1.4426950408889634f
+                 : 0.f;
+    };
+    float next = t < two ? fetch(0) : 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+    for (int i = 0; t < two && i < N; ++i) {
+      const int b = i & 1;
+      gL[b * kTileM + gr] = next;
+      if (i + 1 < N) next = fetch(i + 1);
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+      if (!__all_sync(0xffffffffu, wait_or_abort(&sfull[2 * t + b], (i >> 1) & 1, abort_flag, a.status, 5105))) break;
+      tc_fence_after();
+      const int p0 = (qt0 + i) * a.PT;
+      const bool open = p0 >= key0 + (t + 1) * kTileM - 1 && p0 + a.PT <= len && rows == kTileM;
+      // the columns this key is seen by: first at or after it, last inside the sequence
+      const int c_lo = max(0, key - p0) * a.G, c_hi = min(rows, (len - p0) * a.G);
+#pragma unroll
+      for (int j = 0; j < kTileM; j += 32) {
+        uint32_t v[32];
+        tmem_ld_x32(lane_addr + (2 * t + b) * kTileM + j, v);
+        tmem_wait_ld();
+        const float4* bias = reinterpret_cast<const float4*>(gL + b * kTileM + j);
+        if (open) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            const float4 w = bias[x / 4];
+            const float e0 = ex2f(fmaf(__uint_as_float(v[x]), a.c, -w.x));
+            const float e1 = ex2f(fmaf(__uint_as_float(v[x + 1]), a.c, -w.y));
+            const float e2 = ex2f(fmaf(__uint_as_float(v[x + 2]), a.c, -w.z));
+            const float e3 = ex2f(fmaf(__uint_as_float(v[x + 3]), a.c, -w.w));
+            acc = __fadd2_rn(acc, __fadd2_rn(make_float2(e0, e1), make_float2(e2, e3)));
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const float e = ex2f(fmaf(__uint_as_float(v[x]), a.c, -gL[b * kTileM + j + x]));
+            if (j + x >= c_lo && j + x < c_hi) acc.x += e;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfree[2 * t + b]);
+    }
+    if (t < two && key < len) a.mass[(size_t)(start + key) * a.Hkv + kvh] = acc.x + acc.y;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------
+
+// (D, heads, tokens) map of a [T][heads][D] view with a token stride, in boxes of 64 x heads_box x tokens_box
+int make_map3(CUtensorMap* m, const void* base, bool bf16, int D, int heads, int T, long long stride, int heads_box,
+              int tokens_box) {
+  auto fn = encode_fn();
+  if (!fn) return QE_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)tokens_box};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims,
+         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? QE_OK : QE_ERR_CUDA;
+}
+
+int check_prompt(int B, int T, int Hq, int Hkv, int D, int dtype) {
+  if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return QE_ERR_INVALID_ARG;
+  if (dtype != QE_FP16 && dtype != QE_BF16) return QE_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || Hq / Hkv > QE_MAX_G) return QE_ERR_UNSUPPORTED_SHAPE;
+  // CTAs of a launch, positions of 2 floor(128 / G) each
+  if (((long long)T / 32 + B) * Hkv >= (1ll << 31) || T > (1 << 30)) return QE_ERR_UNSUPPORTED_SHAPE;
+  return QE_OK;
+}
+
+// a [T][heads][D] view: 16-byte aligned, its token stride a multiple of 8 elements that holds a token
+bool view_ok(const void* p, long long stride, int heads, int D) {
+  return p && qe_aligned(p, 16) && stride >= (long long)heads * D && stride % 8 == 0 && stride < (1ll << 38);
+}
+
+template <int D, bool BF16>
+int launch_attend(const void* q, const void* k, const void* v, long long qs, long long ks, long long vs, PromptArgs a,
+                  cudaStream_t st) {
+  using S = AttendSmem<D>;
+  auto kern = prompt_attend_kernel<D, BF16>;
+  static QeOnce once;
+  int dev = 0;
+  int e = qe_once_per_device(once, &dev, [&](int) {
+    QE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES));
+    return QE_OK;
+  });
+  if (e) return e;
+  CUtensorMap tmQ, tmK, tmV;
+  if ((e = make_map3(&tmQ, q, BF16, D, a.Hq, a.T, qs, a.G, a.PT))) return e;
+  if ((e = make_map3(&tmK, k, BF16, D, a.Hkv, a.T, ks, 1, kTileM))) return e;
+  if ((e = make_map3(&tmV, v, BF16, D, a.Hkv, a.T, vs, 1, kTileM))) return e;
+  const int tiles = a.T / (2 * a.PT) + (a.B < a.T ? a.B : a.T);
+  kern<<<tiles * a.Hkv, kPromptThreads, S::BYTES, st>>>(tmQ, tmK, tmV, a);
+  return cudaGetLastError() == cudaSuccess ? QE_OK : QE_ERR_CUDA;
+}
+
+template <int D, bool BF16>
+int launch_mass(const void* q, const void* k, long long qs, long long ks, PromptArgs a, cudaStream_t st) {
+  using S = MassSmem<D>;
+  auto kern = prompt_mass_kernel<D, BF16>;
+  static QeOnce once;
+  int dev = 0;
+  int e = qe_once_per_device(once, &dev, [&](int) {
+    QE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES));
+    return QE_OK;
+  });
+  if (e) return e;
+  CUtensorMap tmQ, tmK;
+  if ((e = make_map3(&tmQ, q, BF16, D, a.Hq, a.T, qs, a.G, a.PT))) return e;
+  if ((e = make_map3(&tmK, k, BF16, D, a.Hkv, a.T, ks, 1, kTileM))) return e;
+  const int tiles = a.T / (2 * kTileM) + (a.B < a.T ? a.B : a.T);
+  kern<<<tiles * a.Hkv, kPromptThreads, S::BYTES, st>>>(tmQ, tmK, a);
+  return cudaGetLastError() == cudaSuccess ? QE_OK : QE_ERR_CUDA;
+}
+
+PromptArgs prompt_args(const int32_t* cu, int B, int T, int Hq, int Hkv, int D, int32_t* status) {
+  PromptArgs a{};
+  a.cu = cu;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.PT = kTileM / a.G;
+  a.c = 1.4426950408889634f / sqrtf((float)D);
+  a.status = status;
+  return a;
+}
+
+}  // namespace
+
+QE_API int qe_prompt_attend(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                            long long v_stride, const int32_t* cu_seqlens, int B, int T, int Hq, int Hkv, int D,
+                            int dtype, void* out, float* lse, int32_t* status, qe_stream_t stream) {
+  const int e = check_prompt(B, T, Hq, Hkv, D, dtype);
+  if (e) return e;
+  if (!cu_seqlens || !status) return QE_ERR_INVALID_ARG;
+  if (T == 0) return QE_OK;
+  if (!view_ok(q, q_stride, Hq, D) || !view_ok(k, k_stride, Hkv, D) || !view_ok(v, v_stride, Hkv, D) || !out ||
+      !qe_aligned(out, 16))
+    return QE_ERR_INVALID_ARG;
+  PromptArgs a = prompt_args(cu_seqlens, B, T, Hq, Hkv, D, status);
+  a.out = out;
+  a.lse = lse;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = dtype == QE_BF16;
+  if (D == 128)
+    return bf ? launch_attend<128, true>(q, k, v, q_stride, k_stride, v_stride, a, st)
+              : launch_attend<128, false>(q, k, v, q_stride, k_stride, v_stride, a, st);
+  return bf ? launch_attend<64, true>(q, k, v, q_stride, k_stride, v_stride, a, st)
+            : launch_attend<64, false>(q, k, v, q_stride, k_stride, v_stride, a, st);
+}
+
+QE_API int qe_prompt_mass(const void* q, const void* k, long long q_stride, long long k_stride, const float* lse,
+                          const int32_t* cu_seqlens, int B, int T, int Hq, int Hkv, int D, int dtype, float* mass,
+                          int32_t* status, qe_stream_t stream) {
+  const int e = check_prompt(B, T, Hq, Hkv, D, dtype);
+  if (e) return e;
+  if (!cu_seqlens || !status) return QE_ERR_INVALID_ARG;
+  if (T == 0) return QE_OK;
+  if (!view_ok(q, q_stride, Hq, D) || !view_ok(k, k_stride, Hkv, D) || !lse || !mass) return QE_ERR_INVALID_ARG;
+  PromptArgs a = prompt_args(cu_seqlens, B, T, Hq, Hkv, D, status);
+  a.lse_in = lse;
+  a.mass = mass;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = dtype == QE_BF16;
+  if (D == 128)
+    return bf ? launch_mass<128, true>(q, k, q_stride, k_stride, a, st)
+              : launch_mass<128, false>(q, k, q_stride, k_stride, a, st);
+  return bf ? launch_mass<64, true>(q, k, q_stride, k_stride, a, st)
+            : launch_mass<64, false>(q, k, q_stride, k_stride, a, st);
+}

@@ -34,6 +34,8 @@ Functions and where they come from (page title, section):
 * ``tier_diagnostics`` / ``future_missed_mass`` -- selection churn, global
   latent importance reactivation and future missed mass; "Resumo Técnico:
   QEvict", Principais Contribuições 1.
+* ``prompt_int4_oracle`` (a module of its own) -- prompt attention, the weight prompt tokens
+  collect, and the 4-bit cache: quantiser, page format, attention, eviction order.
 
 Parity status of each function is listed in ``oracle/qevict_oracle.py``.
 """

@@ -1,0 +1,472 @@
+"""The 4-bit cache on the GPU against float64: entries bit for bit, attention, weights, eviction.
+
+Tolerances of the attention, from the arithmetic: u = eps / 2 of q's dtype, S = max_i sum_d |q| (|c s| +
+|z|) / sqrt(D) over the unit's entries. A score's products are exact (codes times q, the zeros times the
+split sums of q to 2^-22); its additions lose at most D 2^-23 S; the exponent's argument is rounded to
+2^-24 of its size: a weight is off by e_p = (2 D + 8) 2^-24 S + 2^-20 relative.
+- mass: e_p relative per step, plus the float32 addition.
+- out: u |o| for the final rounding; p and p s are each rounded to fp16: 2^-11 sum p |z| + 2^-10 sum p
+  |c s|, with s p >= 2^-28 kept clear of underflow by the factor 16; 2 e_p of the sums.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import prompt_int4_oracle as P
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+
+
+def _cu(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def _draw(seed, shape, dtype, gain=1.0):
+    x = torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+    x[..., 5] *= 8.0
+    return (x * gain).to(DT[dtype]).cuda()
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _scatter(cache, seed=0):
+    """Give the cache's units physical pages in a random order."""
+    n = cache.pages.shape[0]
+    perm = torch.randperm(n, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
+    cache.page_table.copy_(perm.view(cache.units, cache.max_pages))
+
+
+def _filled(lens, Hkv, D, dtype, seed=0, room=0, gain=1.0):
+    """A cache with one prompt a sequence and the oracle's values of its entries."""
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    T = sum(lens)
+    k, v = _draw(seed, (T, Hkv, D), dtype, gain), _draw(seed + 1, (T, Hkv, D), dtype, gain)
+    c = Int4Cache(len(lens), Hkv, D, max(max(lens) + room, 1))
+    _scatter(c, seed)
+    c.pages.fill_(0xff)                        # dead slots hold NaN scales and zeros
+    mass = torch.rand((T, Hkv), generator=torch.Generator().manual_seed(seed + 2)).cuda()
+    c.append(k, v, _cu(lens), mass=mass)
+    return c, k, v, mass
+
+
+def _entries(cache, t, u, n):
+    e = np.arange(n)
+    table = cache.page_table.cpu().numpy()[u]
+    return t.cpu().numpy()[table[e // 16], e % 16]
+
+
+# ---- writing and reading --------------------------------------------------------------
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "fp16"), (128, "bf16"), (64, "fp16")])
+@pytest.mark.parametrize("pieces", [[[1, 1, 1]], [[17, 0, 40]], [[5, 33, 1], [1, 1, 1], [30, 0, 16]]])
+def test_entries_are_bit_exact(D, dtype, pieces):
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    B, Hkv = 3, 2
+    c = Int4Cache(B, Hkv, D, 80)
+    _scatter(c)
+    c.pages.fill_(0xA5)
+    k_all, v_all, m_all = ([[] for _ in range(B)] for _ in range(3))
+    for step, lens in enumerate(pieces):
+        T = sum(lens)
+        k, v = _draw(step, (T, Hkv, D), dtype), _draw(step + 9, (T, Hkv, D), dtype)
+        k[:, 0, :32] = 1.5                                          # a constant group
+        mass = None if step == 1 else torch.rand((T, Hkv)).cuda()
+        c.append(k, v, _cu(lens), mass=mass)
+        for b, (s, n) in enumerate(zip(np.cumsum([0] + lens), lens)):
+            k_all[b].append(_np(k[s:s + n]))
+            v_all[b].append(_np(v[s:s + n]))
+            m_all[b].append(np.zeros((n, Hkv)) if mass is None else _np(mass[s:s + n]))
+    tot = [sum(p[b] for p in pieces) for b in range(B)]
+    assert c.status_word() == (0, 0)
+    assert c.lengths.view(B, Hkv).tolist() == [[n] * Hkv for n in tot] and c.seen.tolist() == tot
+    kr, vr = c.read(_cu(tot), sum(tot), dtype=DT[dtype])
+    table, pages = c.page_table.cpu().numpy(), c.pages.cpu().numpy()
+    s = 0
+    for b in range(B):
+        kb, vb, mb = np.concatenate(k_all[b]), np.concatenate(v_all[b]), np.concatenate(m_all[b])
+        for x, got in ((kb, kr), (vb, vr)):
+            want = torch.from_numpy(P.int4_values(*P.int4_quantize(x)).astype(np.float32)).to(DT[dtype])
+            assert torch.equal(got[s:s + tot[b]].cpu(), want)
+        for h in range(Hkv):
+            u = b * Hkv + h
+            assert _entries(c, c.pos, u, tot[b]).tolist() == list(range(tot[b]))
+            np.testing.assert_array_equal(_entries(c, c.mass, u, tot[b]), mb[:, h].astype(np.float32))
+            for p in range(tot[b] // 16):                               # whole pages, byte for byte
+                np.testing.assert_array_equal(pages[table[u, p]], P.int4_page(kb[16 * p:16 * p + 16, h], vb[16 * p:16 * p + 16, h]))
+        s += tot[b]
+    used = {int(table[b * Hkv + h, p]) for b in range(B) for h in range(Hkv) for p in range(-(-tot[b] // 16))}
+    for p in set(range(len(pages))) - used:
+        assert (pages[p] == 0xA5).all()
+
+
+def test_quantiser_near_ties_and_extremes():
+    """Groups whose quotients fall on and next to half-integers, subnormal scales, the type's range."""
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    D, rows = 64, []
+    for s in (1.0, 0.125, 3.0, 2.0 ** -14, 2.0 ** -24, 1000.0):
+        x = np.arange(64) % 32 * 0.5 * s
+        rows += [x, x - 4 * s, np.nextafter(x.astype(np.float16), np.float16(np.inf)).astype(np.float64)]
+    rows += [np.where(np.arange(64) % 2, 65504.0, -65504.0) * 0.9, np.zeros(64), np.full(64, -3.0)]
+    r = np.random.default_rng(7)
+    rows += list(r.standard_normal((400, 64)) * 10.0 ** r.uniform(-6, 3, (400, 1)))
+    for dtype in ("fp16", "bf16"):
+        x = torch.from_numpy(np.stack(rows)).to(DT[dtype]).cuda().unsqueeze(1)
+        c = Int4Cache(1, 1, D, len(rows))
+        c.append(x, x.flip(0), _cu([len(rows)]))
+        k, v = c.read(_cu([len(rows)]), len(rows), dtype=DT[dtype])
+        want = torch.from_numpy(P.int4_values(*P.int4_quantize(_np(x))).astype(np.float32)).to(DT[dtype])
+        assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want.flip(0))
+
+
+def test_append_strided_rows_outside_sequences_and_read_parts():
+    c, k, v, _ = _filled([40, 21], 2, 64, "bf16", room=40)
+    k0, _ = c.read(_cu([40, 21]), 61)
+    x = _draw(50, (30, 6, 64), "bf16")
+    cu = torch.tensor([4, 10, 12], dtype=torch.int32, device="cuda")       # rows 0-3 and 12.. belong to no one
+    c.append(x[:, 1:3], x[:, 4:6], cu)
+    assert c.lengths.tolist() == [46, 46, 23, 23] and c.seen.tolist() == [46, 23]
+    first = torch.tensor([36, 38, 21, 20], dtype=torch.int32, device="cuda")
+    out = torch.full((14, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    kr, vr = c.read(_cu([9, 5]), 14, first=first, k_out=out, v_out=out.clone())
+    want = torch.from_numpy(P.int4_values(*P.int4_quantize(_np(x[:, 1:3]))).astype(np.float32)).bfloat16().cuda()
+    assert torch.equal(kr[0:4, 0], k0[36:40, 0]) and torch.equal(kr[4:9, 0], want[4:9, 0])
+    assert torch.equal(kr[0:2, 1], k0[38:40, 1]) and torch.equal(kr[2:8, 1][:6], want[4:10, 1][:6])
+    assert (kr[8:9, 1] == 7).all()                                          # entry 46 does not exist
+    assert torch.equal(kr[9:11, 0], want[10:12, 0]) and (kr[11:14, 0] == 7).all()
+
+
+def test_append_refuses_what_does_not_fit_and_bad_pages():
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    x = _draw(1, (20, 1, 64), "bf16")
+    c = Int4Cache(2, 1, 64, 32)
+    c.lengths[1] = 30
+    c.append(x, x, _cu([10, 10]))                       # 30 + 10 entries do not fit unit 1
+    assert c.status_word() == (-3, 1) and c.lengths.tolist() == [10, 30] and c.seen.tolist() == [10, 10]
+    before = c.pages.clone()
+    c.status.zero_()
+    c.page_table[0, 0] = 4                              # n_pages is 4
+    c.append(x[:4], x[:4], _cu([4, 0]))
+    assert c.status_word() == (-7, 0) and torch.equal(c.pages, before)
+    c.status.zero_()
+    c.lengths[0] = -1
+    c.append(x[:4], x[:4], _cu([4, 0]))
+    assert c.status_word() == (-1, 0) and c.lengths.tolist() == [-1, 30]
+    c.status.zero_()
+    c.append(x[:4], x[:4], torch.tensor([0, 3, 2], dtype=torch.int32, device="cuda"))
+    assert c.status_word() == (-1, 1) and torch.equal(c.pages, before)
+
+
+# ---- attention ------------------------------------------------------------------------
+
+
+def _check_attend(c, q, out, before, dtype):
+    """out and the weights of one attend call against float64 over the entries' values."""
+    B, Hq, D = q.shape
+    Hkv, G = c.Hkv, Hq // c.Hkv
+    qn, on = _np(q), _np(out)
+    lens = c.lengths.cpu().numpy()
+    for u in range(c.units):
+        n, b, h = int(lens[u]), u // Hkv, u % Hkv
+        if n == 0:
+            assert (on[b, h * G:(h + 1) * G] == 0).all()
+            continue
+        k, v, ka, vz, vcs = _exact_entries(c, u, n)
+        qq = qn[b, h * G:(h + 1) * G]
+        o, p = P.int4_attend(qq, k, v)
+        S = (ka @ np.abs(qq).T / np.sqrt(D)).max(0)                          # [G]
+        ep = ((2 * D + 8) * S + 16) * 2.0 ** -24
+        A, Z = p.T @ vcs, p.T @ vz
+        tol = U[dtype] * np.abs(o) + 2.0 ** -11 * Z + 2.0 ** -10 * A + 2 * ep[:, None] * (A + Z) + 1e-30
+        err = np.abs(on[b, h * G:(h + 1) * G] - o)
+        assert (err <= tol).all(), (u, n, float((err / tol).max()))
+        if before is not None:
+            w = p.sum(1)
+            got = _entries(c, c.mass, u, n).astype(np.float64) - _entries(c, before, u, n).astype(np.float64)
+            mt = (p * ep).sum(1) + 2.0 ** -23 * (_entries(c, before, u, n) + w)
+            assert (np.abs(got - w) <= mt).all(), (u, n)
+
+
+def _exact_entries(c, u, n):
+    """Float64 values of a unit's entries from its pages' bytes by the documented format; with the
+    magnitudes |c s| + |z| of keys, |z| and c s of values."""
+    D, NG = c.D, c.D // 32
+    pg = c.pages.cpu().numpy()[c.page_table.cpu().numpy()[u]]
+    out = {}
+    ix = np.arange(n)
+    P_, I = ix // 16, ix % 16
+    d = np.arange(D)
+    g, w = d // 32, d % 32
+    halves = pg[:, 16 * D:].copy().view(np.float16).astype(np.float64)
+    kb = I[:, None] * (D // 2) + ((w // 8) * NG + g) * 4 + (w % 8) // 2
+    vb = 8 * D + I[:, None] * (D // 2) + ((w // 4) * NG + g) * 2 + (w % 4) // 2
+    kc = pg[P_[:, None], kb] >> (4 * (d % 2)) & 15
+    vc = pg[P_[:, None], vb] >> (4 * (d % 2)) & 15
+    km = I[:, None] * NG + g
+    vm = ((((I % 8) // 2)[:, None] * NG + g) * 2 + (I // 8)[:, None]) * 2 + (I % 2)[:, None]
+    ks, kz = halves[P_[:, None], km], halves[P_[:, None], D // 2 + km]
+    vs, vz = halves[P_[:, None], D + vm], halves[P_[:, None], 3 * D // 2 + vm]
+    return kc * ks + kz, vc * vs + vz, kc * ks + np.abs(kz), np.abs(vz), vc * vs
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("D,dtype", [(64, "fp16"), (128, "bf16")])
+def test_attend_groups(G, D, dtype):
+    c, *_ = _filled([1, 15, 16, 17, 0, 333], 2, D, dtype, seed=G)
+    q = _draw(77, (6, 2 * G, D), dtype)
+    before = c.mass.clone()
+    out = c.attend(q)
+    assert c.status_word() == (0, 0)
+    _check_attend(c, q, out, before, dtype)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,dtype,gain", [
+    ([1], 1, 1, 128, "fp16", 1.0),
+    ([0, 0], 4, 1, 64, "bf16", 1.0),
+    ([5000, 3, 900], 8, 2, 128, "bf16", 1.0),
+    ([129] * 40, 2, 2, 64, "fp16", 1.0),            # ranges cross many units
+    ([2000, 31], 5, 1, 128, "fp16", 1e-3),          # small values
+    ([700], 8, 1, 64, "bf16", 30.0),                # steep softmax
+])
+def test_attend_lengths(lens, Hq, Hkv, D, dtype, gain):
+    c, *_ = _filled(lens, Hkv, D, dtype, seed=len(lens), gain=gain)
+    q = _draw(78, (len(lens), Hq, D), dtype)
+    out = c.attend(q, accumulate=False)
+    untouched = c.mass.clone()
+    out2 = c.attend(q)
+    assert torch.equal(out, out2) and c.status_word() == (0, 0)
+    _check_attend(c, q, out2, untouched, dtype)
+
+
+def test_attend_query_scales():
+    """Queries of very different sizes per head, zero and tiny ones among them."""
+    c, *_ = _filled([400], 1, 128, "bf16")
+    q = _draw(79, (1, 8, 128), "bf16")
+    q *= torch.tensor([0.0, 1e-30, 1e-6, 1e-3, 1.0, 3.0, 1e-38, 10.0], device="cuda").view(1, 8, 1).bfloat16()
+    before = c.mass.clone()
+    _check_attend(c, q, c.attend(q), before, "bf16")
+
+
+def test_attend_strided_queries_and_repeatability():
+    c, *_ = _filled([500, 77], 2, 64, "fp16")
+    x = _draw(80, (2, 12, 64), "fp16")
+    a = c.attend(x[:, 2:10], accumulate=False)
+    assert torch.equal(a, c.attend(x[:, 2:10].contiguous(), accumulate=False))
+    m0 = c.mass.clone()
+    c.attend(x[:, 2:10])
+    m1 = c.mass.clone()
+    c.mass.copy_(m0)
+    c.attend(x[:, 2:10])
+    assert torch.equal(c.mass, m1)
+
+
+def test_attend_bad_pages_and_lengths():
+    c, *_ = _filled([40, 33], 1, 64, "bf16")
+    good, *_ = _filled([40, 33], 1, 64, "bf16")
+    q = _draw(81, (2, 4, 64), "bf16")
+    want = good.attend(q)
+    c.page_table[0, 1] = -5                              # entries 16..31 of unit 0 count as absent
+    before = c.mass.clone()
+    out = c.attend(q)
+    assert c.status_word() == (-7, 0) and torch.equal(out[1], want[1])
+    k, v, ka, vz, vcs = _exact_entries(good, 0, 40)
+    seen = np.r_[0:16, 32:40]
+    o, p = P.int4_attend(_np(q[0]), k[seen], v[seen])
+    assert np.abs(_np(out[0]) - o).max() <= 0.02 * np.abs(v).max()
+    c.status.zero_()
+    c.page_table[0, 1] = good.page_table[0, 1]
+    c.lengths[0] = 10 ** 6
+    out = c.attend(q)
+    assert c.status_word() == (-1, 0) and (out[0] == 0).all() and torch.equal(out[1], want[1])
+
+
+# ---- eviction -------------------------------------------------------------------------
+
+
+def _check_evict(c, d, budget, recent, untouched):
+    Hkv = c.Hkv
+    sl, seen = c.lengths.cpu().numpy(), c.seen.cpu().numpy()
+    dl = d.lengths.cpu().numpy()
+    assert d.seen.tolist() == c.seen.tolist()
+    dst, dt, dm, dp = d.pages.cpu().numpy(), d.page_table.cpu().numpy(), d.mass.cpu().numpy(), d.pos.cpu().numpy()
+    live = np.zeros(dm.shape, bool)
+    for u in range(c.units):
+        n = int(sl[u])
+        m, p = _entries(c, c.mass, u, n), _entries(c, c.pos, u, n)
+        keep = P.int4_evict(m, p, seen[u // Hkv], budget, recent)
+        assert dl[u] == len(keep), u
+        e = np.arange(len(keep))
+        pg = dt[u][e // 16]
+        live[pg, e % 16] = True
+        np.testing.assert_array_equal(dm[pg, e % 16], m[keep])
+        np.testing.assert_array_equal(dp[pg, e % 16], p[keep])
+        if len(keep):
+            a, b = _exact_entries(c, u, n), _exact_entries(d, u, len(keep))
+            for x, y in zip(a, b):
+                np.testing.assert_array_equal(x[keep], y)
+    assert (dm[~live] == untouched).all() and (dp[~live] == 7).all()
+    dead = ~live.any(1)
+    assert (dst[dead] == 0x3C).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,budget,recent", [
+    ([1], 1, 0), ([33, 0, 17], 16, 4), ([100, 5], 5, 5), ([2000, 300], 777, 100), ([2064, 2048], 2048, 256),
+    ([5000], 1, 1), ([1300], 1299, 0), ([70], 64, 64)])
+def test_evict(D, lens, budget, recent):
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    c, *_ = _filled(lens, 2, D, "bf16", seed=budget)
+    r = torch.Generator().manual_seed(budget)
+    w = torch.rand(c.mass.shape, generator=r)
+    w = torch.where(w < 0.2, torch.zeros(()), torch.where(w < 0.3, torch.full((), 0.5), w))     # many ties
+    c.mass.copy_(w)
+    d = Int4Cache(len(lens), 2, D, budget)
+    _scatter(d, 3)
+    d.pages.fill_(0x3C)
+    d.mass.fill_(-9.0)
+    d.pos.fill_(7)
+    d.lengths.fill_(99)
+    src = [t.clone() for t in (c.pages, c.mass, c.pos, c.counts)]
+    c.evict(d, budget, recent)
+    assert c.status_word() == (0, 0) and d.status_word() == (0, 0)
+    for a, b in zip(src, (c.pages, c.mass, c.pos, c.counts)):
+        assert torch.equal(a, b)
+    _check_evict(c, d, budget, recent, -9.0)
+
+
+def test_evict_odd_weights():
+    """NaN, infinities, both zeros and negative weights order as documented."""
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    c, *_ = _filled([64], 1, 64, "fp16")
+    odd = [float("nan"), float("inf"), -float("inf"), 0.0, -0.0, -1.0, 1e-40, 3.4e38]
+    c.mass.copy_(torch.tensor(odd * 8).view(4, 16))
+    for budget in (1, 8, 9, 20, 33, 50, 57, 63):
+        d = Int4Cache(1, 1, 64, budget)
+        d.mass.fill_(-9.0)
+        d.pos.fill_(7)
+        d.pages.fill_(0x3C)
+        c.evict(d, budget, 0)
+        _check_evict(c, d, budget, 0, -9.0)
+
+
+def test_evict_bad_state():
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    c, *_ = _filled([64, 64], 1, 64, "fp16")
+    d = Int4Cache(2, 1, 64, 32)
+    c.lengths[0] = 65
+    c.evict(d, 32, 0)
+    assert c.status_word() == (-1, 0) and d.lengths.tolist() == [0, 32]
+    c.status.zero_()
+    c.lengths[0] = 64
+    d.page_table[1, 0] = 99
+    c.evict(d, 32, 0)
+    assert c.status_word() == (0, 0) and d.status_word() == (-7, 1)
+    c.page_table[0, 2] = -1
+    c.evict(Int4Cache(2, 1, 64, 64), 64, 0)
+    assert c.status_word() == (-7, 0)
+
+
+# ---- together -------------------------------------------------------------------------
+
+
+def test_prompt_then_decode_with_eviction():
+    """A prompt is attended, its weights and 4-bit entries cached and cut to the budget; decode steps append,
+    attend and every fourth step evict into the other of two caches. Every step's output and weights are
+    checked against float64 over the entries the cache holds."""
+    from kv_cache_eviction_gqa_b200 import binding as B
+    lens, Hq, Hkv, D, budget, recent, every = [300, 45, 1], 8, 2, 128, 64, 16, 4
+    x = _draw(90, (sum(lens), Hq + 2 * Hkv, D), "bf16")
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    cu = _cu(lens)
+    _, lse, status = B.prompt_attend(q, k, v, cu)
+    mass, _ = B.prompt_mass(q, k, lse, cu, status=status)
+    big = B.Int4Cache(3, Hkv, D, max(lens))
+    big.append(k, v, cu, mass=mass)
+    cur, spare = (B.Int4Cache(3, Hkv, D, budget + every) for _ in range(2))
+    _scatter(cur, 1)
+    _scatter(spare, 2)
+    big.evict(cur, budget, recent)
+    assert cur.lengths.view(3, Hkv).tolist() == [[64] * 2, [45] * 2, [1] * 2]
+    one = _cu([1, 1, 1])
+    for step in range(12):
+        y = _draw(100 + step, (3, Hq + 2 * Hkv, D), "bf16")
+        cur.append(y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], one)
+        before = cur.mass.clone()
+        out = cur.attend(y[:, :Hq])
+        _check_attend(cur, y[:, :Hq], out, before, "bf16")
+        if step % every == every - 1:
+            for t in (spare.pos, spare.mass):
+                t.fill_(7)
+            spare.pages.fill_(0x3C)
+            cur.evict(spare, budget, recent)
+            _check_evict(cur, spare, budget, recent, 7)
+            cur, spare = spare, cur
+    assert cur.seen.tolist() == [n + 12 for n in lens] and int(cur.lengths.max()) == budget
+    for c in (big, cur, spare):
+        assert c.status_word() == (0, 0)
+    assert status.tolist() == [0, 0]
+
+
+def test_captured_step_with_two_caches_and_streams():
+    """A captured append + attend replays on what the tensors then hold; two caches, each with its scratch,
+    step on two streams at once."""
+    from kv_cache_eviction_gqa_b200 import binding as B
+    caches, refs = [], []
+    for s in range(2):
+        caches.append(_filled([700, 90], 2, 128, "bf16", seed=5 + s, room=20)[0])
+        refs.append(_filled([700, 90], 2, 128, "bf16", seed=5 + s, room=20)[0])
+    one = _cu([1, 1])
+    ys = [torch.empty((2, 12, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    outs = [torch.empty((2, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    graphs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for s in range(2):
+        caches[s].scratch(8)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[s]):
+            caches[s].append(ys[s][:, 8:10], ys[s][:, 10:], one)
+            caches[s].attend(ys[s][:, :8], out=outs[s])
+        graphs.append(g)
+    for step in range(5):
+        for s in range(2):
+            ys[s].copy_(_draw(200 + 2 * step + s, (2, 12, 128), "bf16"))
+        torch.cuda.synchronize()
+        for s in range(2):
+            with torch.cuda.stream(streams[s]):
+                graphs[s].replay()
+        torch.cuda.synchronize()
+        for s in range(2):
+            refs[s].append(ys[s][:, 8:10], ys[s][:, 10:], one)
+            want = refs[s].attend(ys[s][:, :8])
+            assert torch.equal(outs[s], want) and torch.equal(caches[s].mass, refs[s].mass)
+            assert torch.equal(caches[s].counts, refs[s].counts)
+
+
+def test_binding_refusals():
+    from kv_cache_eviction_gqa_b200 import binding as B
+    c, k, v, mass = _filled([20], 2, 64, "bf16")
+    with pytest.raises(ValueError):
+        c.append(k, v.half(), _cu([20]))
+    with pytest.raises(ValueError):
+        c.append(k, v, _cu([10, 10]))
+    with pytest.raises(ValueError):
+        c.append(k, v, _cu([20]), mass=mass.double())
+    with pytest.raises(ValueError):
+        c.attend(k[:2, :2])                                # two rows for one sequence
+    with pytest.raises(ValueError):
+        c.attend(k[:1].float())
+    with pytest.raises(ValueError):
+        c.read(_cu([20]), 20, first=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(RuntimeError, match="invalid"):
+        c.evict(c, 4, 0)
+    with pytest.raises(RuntimeError, match="invalid"):
+        c.evict(B.Int4Cache(1, 2, 64, 16), 17, 0)
+    with pytest.raises(RuntimeError, match="invalid"):
+        c.evict(B.Int4Cache(1, 1, 64, 16), 16, 0)
