@@ -456,8 +456,8 @@ QE_API int qe_prompt_mass(const void* q, const void* k, long long q_stride, long
  *     length out of range, detail = the unit, which counts as empty; bounds out of order, detail =
  *     the sequence, nothing is done), QE_ERR_POOL_EXHAUSTED (an append that does not fit, detail =
  *     the unit, which stays as it was), QE_ERR_DEVICE_FAULT (a page-table entry outside [0, n_pages),
- *     detail = the unit; its entries count as absent), QE_ERR_TIMEOUT. The third word is the
- *     library's own. One call at a time may use a cache. */
+ *     detail = the unit; its entries count as absent), QE_ERR_TIMEOUT. The words from the third on
+ *     are the library's own. One call at a time may use a cache. */
 typedef struct {
   int B, Hkv, D;            /* sequences, kv heads, head dim (64 or 128)          */
   int max_pages;            /* entries of a unit's page-table row                 */
@@ -466,9 +466,9 @@ typedef struct {
   int32_t* page_table;      /* [dev] [B * Hkv][max_pages]                         */
   int32_t* lengths;         /* [dev] [B * Hkv] live entries of each unit          */
   int32_t* seen;            /* [dev] [B] tokens appended to each sequence so far  */
-  float* mass;              /* [dev] [n_pages][16] weight collected by each entry */
-  int32_t* pos;             /* [dev] [n_pages][16] position of each entry         */
-  int32_t* status;          /* [dev] [4]                                          */
+  float* mass;              /* [dev] [n_pages][16] weight of each entry, 16-byte aligned */
+  int32_t* pos;             /* [dev] [n_pages][16] position of each entry, 16-byte aligned */
+  int32_t* status;          /* [dev] [64 + 2 * B * Hkv]                           */
 } qe_int4_cache;
 
 /* qe_int4_append - quantise new tokens into the cache: a prompt, or one token a sequence.

@@ -8,6 +8,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -612,8 +613,21 @@ def _tokens(t: torch.Tensor, name: str, heads: int, D: int, dtype, T=None) -> in
 
 def _same_device(dev, *named):
     for t, name in named:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev.index:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev):
+    """The context in which calls go to dev (nothing to do when it is the current device)."""
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _raw(stream, dev) -> int:
+    """The CUDA stream of a torch stream, by default the current one of dev."""
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
 
 
 def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, out=None, lse=None,
@@ -632,17 +646,17 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     ks = _tokens(k, "k", Hkv, D, q.dtype, T)
     vs = _tokens(v, "v", Hkv, D, q.dtype, T)
     _need(cu_seqlens, "cu_seqlens", torch.int32)
-    with torch.cuda.device(dev):
+    with _on(dev):
         out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None else lse
         status = torch.zeros(2, dtype=torch.int32, device=dev) if status is None else status
         _need(out, "out", q.dtype, (T, Hq, D))
         _need(lse, "lse", torch.float32, (T, Hq))
-        _need(status, "status", torch.int32)
+        _need(status, "status", torch.int32, (2,))
         _same_device(dev, (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens"), (out, "out"), (lse, "lse"), (status, "status"))
-        _check(lib().qe_prompt_attend(_ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(cu_seqlens), cu_seqlens.numel() - 1,
-                                      T, Hq, Hkv, D, dtype_code(q.dtype), _ptr(out), _ptr(lse), _ptr(status),
-                                      _stream(stream)), "qe_prompt_attend")
+        _check(lib().qe_prompt_attend(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_seqlens.data_ptr(),
+                                      cu_seqlens.numel() - 1, T, Hq, Hkv, D, dtype_code(q.dtype), out.data_ptr(),
+                                      lse.data_ptr(), status.data_ptr(), _raw(stream, dev)), "qe_prompt_attend")
     return out, lse, status
 
 
@@ -657,14 +671,14 @@ def prompt_mass(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_seqlens:
     ks = _tokens(k, "k", Hkv, D, q.dtype, T)
     _need(cu_seqlens, "cu_seqlens", torch.int32)
     _need(lse, "lse", torch.float32, (T, Hq))
-    with torch.cuda.device(dev):
+    with _on(dev):
         mass = torch.empty((T, Hkv), dtype=torch.float32, device=dev) if mass is None else mass
         status = torch.zeros(2, dtype=torch.int32, device=dev) if status is None else status
         _need(mass, "mass", torch.float32, (T, Hkv))
-        _need(status, "status", torch.int32)
+        _need(status, "status", torch.int32, (2,))
         _same_device(dev, (k, "k"), (lse, "lse"), (cu_seqlens, "cu_seqlens"), (mass, "mass"), (status, "status"))
-        _check(lib().qe_prompt_mass(_ptr(q), _ptr(k), qs, ks, _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T,
-                                    Hq, Hkv, D, dtype_code(q.dtype), _ptr(mass), _ptr(status), _stream(stream)),
+        _check(lib().qe_prompt_mass(q.data_ptr(), k.data_ptr(), qs, ks, lse.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T,
+                                    Hq, Hkv, D, dtype_code(q.dtype), mass.data_ptr(), status.data_ptr(), _raw(stream, dev)),
                "qe_prompt_mass")
     return mass, status
 
@@ -692,7 +706,7 @@ class Int4Cache:
         self.lengths, self.seen = self.counts[:self.units], self.counts[self.units:]
         self.mass = torch.zeros((n, 16), dtype=torch.float32, device=device)
         self.pos = torch.zeros((n, 16), dtype=torch.int32, device=device)
-        self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self.status = torch.zeros(64 + 2 * self.units, dtype=torch.int32, device=device)
         self._scratch = {}
         self._c = QeInt4Cache(B, Hkv, D, self.max_pages, n, *(t.data_ptr() for t in (
             self.pages, self.page_table, self.lengths, self.seen, self.mass, self.pos, self.status)))
@@ -712,9 +726,9 @@ class Int4Cache:
         if mass is not None:
             _need(mass, "mass", torch.float32, (T, self.Hkv))
         _same_device(self.device, (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens"), (mass, "mass"))
-        with torch.cuda.device(self.device):
-            _check(lib().qe_int4_append(C.byref(self._c), _ptr(k), _ptr(v), ks, vs, _ptr(cu_seqlens), T,
-                                        dtype_code(k.dtype), None if mass is None else _ptr(mass), _stream(stream)),
+        with _on(self.device):
+            _check(lib().qe_int4_append(C.byref(self._c), k.data_ptr(), v.data_ptr(), ks, vs, cu_seqlens.data_ptr(), T,
+                                        dtype_code(k.dtype), None if mass is None else mass.data_ptr(), _raw(stream, self.device)),
                    "qe_int4_append")
 
     def read(self, cu_seqlens: torch.Tensor, T: int, first=None, dtype=torch.bfloat16, k_out=None, v_out=None,
@@ -725,14 +739,14 @@ class Int4Cache:
         _need(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,))
         if first is not None:
             _need(first, "first", torch.int32, (self.units,))
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             k_out = torch.empty(shape, dtype=dtype, device=self.device) if k_out is None else k_out
             v_out = torch.empty(shape, dtype=dtype, device=self.device) if v_out is None else v_out
             _need(k_out, "k_out", dtype, shape)
             _need(v_out, "v_out", dtype, shape)
             _same_device(self.device, (cu_seqlens, "cu_seqlens"), (first, "first"), (k_out, "k_out"), (v_out, "v_out"))
-            _check(lib().qe_int4_read(C.byref(self._c), _ptr(cu_seqlens), T, None if first is None else _ptr(first),
-                                      dtype_code(dtype), _ptr(k_out), _ptr(v_out), _stream(stream)), "qe_int4_read")
+            _check(lib().qe_int4_read(C.byref(self._c), cu_seqlens.data_ptr(), T, None if first is None else first.data_ptr(),
+                                      dtype_code(dtype), k_out.data_ptr(), v_out.data_ptr(), _raw(stream, self.device)), "qe_int4_read")
         return k_out, v_out
 
     def scratch(self, Hq: int) -> torch.Tensor:
@@ -752,20 +766,20 @@ class Int4Cache:
         if B != self.B or D != self.D:
             raise ValueError(f"q must be [{self.B}][Hq][{self.D}], got {tuple(q.shape)}")
         qs = _tokens(q, "q", Hq, D, q.dtype)
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             out = torch.empty((B, Hq, D), dtype=q.dtype, device=self.device) if out is None else out
             _need(out, "out", q.dtype, (B, Hq, D))
             scratch = self.scratch(Hq) if scratch is None else scratch
             _same_device(self.device, (q, "q"), (out, "out"), (scratch, "scratch"))
-            _check(lib().qe_int4_attend(C.byref(self._c), _ptr(q), qs, Hq, dtype_code(q.dtype), int(accumulate),
-                                        _ptr(out), _ptr(scratch), scratch.numel(), _stream(stream)), "qe_int4_attend")
+            _check(lib().qe_int4_attend(C.byref(self._c), q.data_ptr(), qs, Hq, dtype_code(q.dtype), int(accumulate),
+                                        out.data_ptr(), scratch.data_ptr(), scratch.numel(), _raw(stream, self.device)), "qe_int4_attend")
         return out
 
     def evict(self, into: "Int4Cache", budget: int, recent: int, stream=None) -> "Int4Cache":
         """Copy each unit's `recent` newest entries and the heaviest others, `budget` in all, into
         another cache (its lengths, weights and positions are written; this one stays as it was)."""
         _same_device(self.device, (into.pages, "into"))
-        with torch.cuda.device(self.device):
-            _check(lib().qe_int4_evict(C.byref(self._c), C.byref(into._c), budget, recent, _stream(stream)),
+        with _on(self.device):
+            _check(lib().qe_int4_evict(C.byref(self._c), C.byref(into._c), budget, recent, _raw(stream, self.device)),
                    "qe_int4_evict")
         return into

@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
 struct RowArgs {
   const void* k;
@@ -47,81 +47,122 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t) {
   return lo;
 }
 
-// An item is one token of one kv head, a key row and a value row of D elements: D / 4 lanes take
-// four consecutive elements of each, so a group of 32 is eight lanes.
+// 16-bit pairs: maxima and minima are exact, and half as many instructions as in float32
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __half) {
+  const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __nv_bfloat16) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// (max x, max -x) over the eight lanes of a group for each of eight rows, lane i % 8 keeping row i: three
+// exchanges in which each lane gives away the half of the rows that it does not keep
+template <typename T>
+__device__ __forceinline__ uint32_t group_ranges(const uint2 (&w)[8], int lane) {
+  constexpr uint32_t kSigns = 0x80008000u;
+  uint32_t m[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const uint32_t a = max2(w[x].x, w[x].y, T()), n = max2(w[x].x ^ kSigns, w[x].y ^ kSigns, T());
+    m[x] = max2(__byte_perm(a, n, 0x5410), __byte_perm(a, n, 0x7632), T());
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int x = 0; x < o; ++x) {
+      const uint32_t give = up ? m[x] : m[x + o], keep = up ? m[x + o] : m[x];
+      m[x] = max2(keep, __shfl_xor_sync(0xffffffffu, give, o), T());
+    }
+  }
+  return m[0];
+}
+
+// A warp takes eight row slots of one kv head (D = 128: eight tokens, 32 lanes a row of four elements
+// each; D = 64: sixteen tokens, half a warp a row), so that look-ups (which sequence, which page)
+// are done by lanes side by side, all rows' loads are in flight together, and of the eight lanes that
+// hold a group each works out scale and zero of one row.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) int4_append_kernel(Int4View c, RowArgs a) {
-  constexpr int LPI = D / 4, NG = D / 32, IPB = kRowThreads / LPI;
-  __shared__ int s_ok;
+  constexpr int LPI = D / 4, NG = D / 32, PER = 32 / LPI, TILE = 8 * PER;
+  __shared__ int s_ok, s_last;
+  const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
     const bool ok = bounds_ok(a.cu, c.B, a.T, c.status);
     if (threadIdx.x == 0) s_ok = ok;
   }
   __syncthreads();
   if (!s_ok) return;
-  const int sub = threadIdx.x / LPI, l = threadIdx.x % LPI, g = l / 8, e8 = l % 8;
-  const long long items = (long long)a.T * c.Hkv;
-  for (long long it0 = (long long)blockIdx.x * IPB; it0 < items; it0 += (long long)gridDim.x * IPB) {
-    const long long it = it0 + sub;
-    const bool live = it < items;
-    const int t = live ? (int)(it / c.Hkv) : 0, h = live ? (int)(it % c.Hkv) : 0;
-    float k[4] = {}, v[4] = {};
-    if (live) {
-      const uint2 kw = *reinterpret_cast<const uint2*>(static_cast<const T*>(a.k) + t * a.ks + h * D + 4 * l);
-      const uint2 vw = *reinterpret_cast<const uint2*>(static_cast<const T*>(a.v) + t * a.vs + h * D + 4 * l);
-      k[0] = Elem<T>::lo(kw.x), k[1] = Elem<T>::hi(kw.x), k[2] = Elem<T>::lo(kw.y), k[3] = Elem<T>::hi(kw.y);
-      v[0] = Elem<T>::lo(vw.x), v[1] = Elem<T>::hi(vw.x), v[2] = Elem<T>::lo(vw.y), v[3] = Elem<T>::hi(vw.y);
-    }
-    float kmn = fminf(fminf(k[0], k[1]), fminf(k[2], k[3])), kmx = fmaxf(fmaxf(k[0], k[1]), fmaxf(k[2], k[3]));
-    float vmn = fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), vmx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+  const int l = lane % LPI, g = l / 8, e8 = l % 8, half = lane / LPI;
+  const int tiles = (a.T + TILE - 1) / TILE;
+  const long long items = (long long)tiles * c.Hkv;
+  for (long long it = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += (long long)gridDim.x * (kRowThreads / 32)) {
+    // slot x of this half warp is token t0 + 8 half + x
+    const int t0 = (int)(it / c.Hkv) * TILE, h = (int)(it % c.Hkv), rows = min(TILE, a.T - t0);
+    uint2 kw[8], vw[8];
+    const T* ks = static_cast<const T*>(a.k) + (t0 + 8 * half) * a.ks + h * D + 4 * l;
+    const T* vs = static_cast<const T*>(a.v) + (t0 + 8 * half) * a.vs + h * D + 4 * l;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      kmn = fminf(kmn, __shfl_xor_sync(0xffffffffu, kmn, o));
-      kmx = fmaxf(kmx, __shfl_xor_sync(0xffffffffu, kmx, o));
-      vmn = fminf(vmn, __shfl_xor_sync(0xffffffffu, vmn, o));
-      vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, o));
+    for (int x = 0; x < 8; ++x) {
+      kw[x] = vw[x] = make_uint2(0, 0);
+      if (8 * half + x < rows) {
+        kw[x] = __ldcs(reinterpret_cast<const uint2*>(ks + x * a.ks));
+        vw[x] = __ldcs(reinterpret_cast<const uint2*>(vs + x * a.vs));
+      }
     }
-    if (!live) continue;
-    const int b = sequence_of(a.cu, c.B, t);
-    if (b < 0) continue;                                  // rows outside every sequence
-    const int u = b * c.Hkv + h, n = a.cu[b + 1] - a.cu[b], j = t - a.cu[b];
-    const int len = c.lengths[u];
-    if (len < 0 || (long long)len + n > (long long)c.max_pages * kInt4Page) {
-      if (l == 0) qe_record_error(c.status, len < 0 ? QE_ERR_INVALID_ARG : QE_ERR_POOL_EXHAUSTED, u);
-      continue;
+    // lane r < TILE: where token t0 + r goes
+    int page = -1, slot = 0;
+    if (lane < rows) {
+      const int t = t0 + lane, b = sequence_of(a.cu, c.B, t);
+      if (b >= 0) {                                       // else a row outside every sequence
+        const int u = b * c.Hkv + h, s = a.cu[b], n = a.cu[b + 1] - s, len = c.lengths[u];
+        if (len < 0 || (long long)len + n > (long long)c.max_pages * kInt4Page) {
+          qe_record_error(c.status, len < 0 ? QE_ERR_INVALID_ARG : QE_ERR_POOL_EXHAUSTED, u);
+        } else {
+          const int e = len + t - s;
+          page = c.table[(size_t)u * c.max_pages + e / kInt4Page];
+          slot = e % kInt4Page;
+          if (page < 0 || page >= c.n_pages) {
+            qe_record_error(c.status, QE_ERR_DEVICE_FAULT, u);
+            page = -1;
+          } else {
+            const size_t at = (size_t)page * kInt4Page + slot;
+            c.mass[at] = a.mass ? a.mass[(size_t)t * c.Hkv + h] : 0.f;
+            c.pos[at] = c.seen[b] + t - s;
+          }
+        }
+      }
     }
-    const int e = len + j, i = e % kInt4Page;
-    const int page = c.table[(size_t)u * c.max_pages + e / kInt4Page];
-    if (page < 0 || page >= c.n_pages) {
-      if (l == 0) qe_record_error(c.status, QE_ERR_DEVICE_FAULT, u);
-      continue;
+    const uint32_t kr = group_ranges<T>(kw, lane), vr = group_ranges<T>(vw, lane);
+    const uint32_t km = int4_meta(-Elem<T>::hi(kr), Elem<T>::lo(kr)), vm = int4_meta(-Elem<T>::hi(vr), Elem<T>::lo(vr));
+    const float ki = int4_inv15(km), vi = int4_inv15(vm);
+    {                                                     // this lane's row and group: its four halves
+      const int pg_i = __shfl_sync(0xffffffffu, page, 8 * half + e8), i = __shfl_sync(0xffffffffu, slot, 8 * half + e8);
+      if (pg_i >= 0) {
+        uint16_t* m = reinterpret_cast<uint16_t*>(c.pages + (size_t)pg_i * (20 * D) + 16 * D);
+        const int mk = i * NG + g, mv = ((((i & 7) >> 1) * NG + g) * 2 + (i >> 3)) * 2 + (i & 1);
+        m[mk] = (uint16_t)km, m[D / 2 + mk] = (uint16_t)(km >> 16);
+        m[D + mv] = (uint16_t)vm, m[3 * D / 2 + mv] = (uint16_t)(vm >> 16);
+      }
     }
-    const Int4Group kg(kmn, kmx), vg(vmn, vmx);
-    uint32_t kc = 0, vc = 0;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      kc |= kg.code(k[x]) << (4 * x);
-      vc |= vg.code(v[x]) << (4 * x);
-    }
-    uint8_t* pg = c.pages + (size_t)page * (20 * D);
-    *reinterpret_cast<uint16_t*>(pg + i * (D / 2) + ((e8 >> 1) * NG + g) * 4 + (e8 & 1) * 2) = (uint16_t)kc;
-    *reinterpret_cast<uint16_t*>(pg + 8 * D + i * (D / 2) + (e8 * NG + g) * 2) = (uint16_t)vc;
-    if (e8 == 0) {
-      __half* m = reinterpret_cast<__half*>(pg + 16 * D);
-      const int km = i * NG + g, vm = ((((i & 7) >> 1) * NG + g) * 2 + (i >> 3)) * 2 + (i & 1);
-      m[km] = kg.sh;
-      m[D / 2 + km] = kg.zh;
-      m[D + vm] = vg.sh;
-      m[3 * D / 2 + vm] = vg.zh;
-    }
-    if (l == 0) {
-      const size_t at = (size_t)page * kInt4Page + i;
-      c.mass[at] = a.mass ? a.mass[(size_t)t * c.Hkv + h] : 0.f;
-      c.pos[at] = c.seen[b] + j;
+    for (int x = 0; x < 8; ++x) {
+      const int pg_i = __shfl_sync(0xffffffffu, page, 8 * half + x), i = __shfl_sync(0xffffffffu, slot, 8 * half + x);
+      const int from = (lane & ~7) | x;
+      const uint32_t mk = __shfl_sync(0xffffffffu, km, from), mv = __shfl_sync(0xffffffffu, vm, from);
+      const float ik = __shfl_sync(0xffffffffu, ki, from), iv = __shfl_sync(0xffffffffu, vi, from);
+      const uint32_t kc = int4_codes(Elem<T>::lo(kw[x].x), Elem<T>::hi(kw[x].x), Elem<T>::lo(kw[x].y), Elem<T>::hi(kw[x].y), mk, ik);
+      const uint32_t vc = int4_codes(Elem<T>::lo(vw[x].x), Elem<T>::hi(vw[x].x), Elem<T>::lo(vw[x].y), Elem<T>::hi(vw[x].y), mv, iv);
+      if (pg_i < 0) continue;
+      uint8_t* pg = c.pages + (size_t)pg_i * (20 * D) + i * (D / 2);
+      *reinterpret_cast<uint16_t*>(pg + ((e8 >> 1) * NG + g) * 4 + (e8 & 1) * 2) = (uint16_t)kc;
+      *reinterpret_cast<uint16_t*>(pg + 8 * D + (e8 * NG + g) * 2) = (uint16_t)vc;
     }
   }
   // the last CTA to finish moves the lengths on: every other one has read them
-  __shared__ int s_last;
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
@@ -137,47 +178,75 @@ __global__ void __launch_bounds__(kRowThreads) int4_append_kernel(Int4View c, Ro
   if (threadIdx.x == 0) c.status[2] = 0;
 }
 
+// The values of a tile of rows of one kv head a warp, look-ups as above; D / 8 lanes hold a row, eight
+// elements each.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) int4_read_kernel(Int4View c, RowArgs a) {
-  constexpr int LPI = D / 4, NG = D / 32, IPB = kRowThreads / LPI;
+  constexpr int LPI = D / 8, NG = D / 32, PER = 32 / LPI, TILE = 8 * (128 / D), STEPS = TILE / PER;
   __shared__ int s_ok;
+  const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
     const bool ok = bounds_ok(a.cu, c.B, a.T, c.status);
     if (threadIdx.x == 0) s_ok = ok;
   }
   __syncthreads();
   if (!s_ok) return;
-  const int sub = threadIdx.x / LPI, l = threadIdx.x % LPI, g = l / 8, e8 = l % 8;
-  const long long items = (long long)a.T * c.Hkv;
-  for (long long it = (long long)blockIdx.x * IPB + sub; it < items; it += (long long)gridDim.x * IPB) {
-    const int t = (int)(it / c.Hkv), h = (int)(it % c.Hkv);
-    const int b = sequence_of(a.cu, c.B, t);
-    if (b < 0) continue;
-    const int u = b * c.Hkv + h;
-    const long long e = (long long)(a.first ? a.first[u] : 0) + t - a.cu[b];
-    if (e < 0 || e >= c.lengths[u] || e >= (long long)c.max_pages * kInt4Page) continue;   // no such entry
-    const int i = (int)(e % kInt4Page), page = c.table[(size_t)u * c.max_pages + e / kInt4Page];
-    if (page < 0 || page >= c.n_pages) {
-      if (l == 0) qe_record_error(c.status, QE_ERR_DEVICE_FAULT, u);
-      continue;
+  const int l = lane % LPI, g = l / 4, t4 = l % 4;
+  const int tiles = (a.T + TILE - 1) / TILE;
+  const long long items = (long long)tiles * c.Hkv;
+  for (long long it = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += (long long)gridDim.x * (kRowThreads / 32)) {
+    const int t0 = (int)(it / c.Hkv) * TILE, h = (int)(it % c.Hkv), rows = min(TILE, a.T - t0);
+    int page = -1, slot = 0;
+    if (lane < rows) {
+      const int t = t0 + lane, b = sequence_of(a.cu, c.B, t);
+      if (b >= 0) {
+        const int u = b * c.Hkv + h;
+        const long long e = (long long)(a.first ? a.first[u] : 0) + t - a.cu[b];
+        if (e >= 0 && e < c.lengths[u] && e < (long long)c.max_pages * kInt4Page) {   // else no such entry
+          page = c.table[(size_t)u * c.max_pages + e / kInt4Page];
+          slot = (int)(e % kInt4Page);
+          if (page < 0 || page >= c.n_pages) {
+            qe_record_error(c.status, QE_ERR_DEVICE_FAULT, u);
+            page = -1;
+          }
+        }
+      }
     }
-    const uint8_t* pg = c.pages + (size_t)page * (20 * D);
-    const uint32_t kc = *reinterpret_cast<const uint16_t*>(pg + i * (D / 2) + ((e8 >> 1) * NG + g) * 4 + (e8 & 1) * 2);
-    const uint32_t vc = *reinterpret_cast<const uint16_t*>(pg + 8 * D + i * (D / 2) + (e8 * NG + g) * 2);
-    const __half* m = reinterpret_cast<const __half*>(pg + 16 * D);
-    const int km = i * NG + g, vm = ((((i & 7) >> 1) * NG + g) * 2 + (i >> 3)) * 2 + (i & 1);
-    const float ksc = __half2float(m[km]), kz = __half2float(m[D / 2 + km]);
-    const float vsc = __half2float(m[D + vm]), vz = __half2float(m[3 * D / 2 + vm]);
-    // c s is exact in float32; the sum is rounded to float32, then to the output type
-    T ko[4], vo[4];
+    uint32_t kc[STEPS], vc[STEPS], km[STEPS], vm[STEPS];
+    int has = 0;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      ko[x] = Elem<T>::from_f(fmaf((float)(kc >> (4 * x) & 15u), ksc, kz));
-      vo[x] = Elem<T>::from_f(fmaf((float)(vc >> (4 * x) & 15u), vsc, vz));
+    for (int x = 0; x < STEPS; ++x) {
+      const int r = x * PER + lane / LPI;
+      const int pg_i = __shfl_sync(0xffffffffu, page, r), i = __shfl_sync(0xffffffffu, slot, r);
+      kc[x] = vc[x] = km[x] = vm[x] = 0u;
+      if (pg_i < 0) continue;
+      has |= 1 << x;
+      const uint8_t* pg = c.pages + (size_t)pg_i * (20 * D);
+      const uint16_t* vr = reinterpret_cast<const uint16_t*>(pg + 8 * D + i * (D / 2)) + 2 * t4 * NG + g;
+      const uint16_t* m = reinterpret_cast<const uint16_t*>(pg + 16 * D);
+      const int mk = i * NG + g, mv = ((((i & 7) >> 1) * NG + g) * 2 + (i >> 3)) * 2 + (i & 1);
+      kc[x] = *reinterpret_cast<const uint32_t*>(pg + i * (D / 2) + (t4 * NG + g) * 4);
+      vc[x] = vr[0] | (uint32_t)vr[NG] << 16;
+      km[x] = m[mk] | (uint32_t)m[D / 2 + mk] << 16;
+      vm[x] = m[D + mv] | (uint32_t)m[3 * D / 2 + mv] << 16;
     }
-    const size_t o = ((size_t)t * c.Hkv + h) * D + 4 * l;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.k_out) + o) = *reinterpret_cast<uint2*>(ko);
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.v_out) + o) = *reinterpret_cast<uint2*>(vo);
+#pragma unroll
+    for (int x = 0; x < STEPS; ++x) {
+      if (!(has >> x & 1)) continue;
+      const int r = x * PER + lane / LPI;
+      // c s is exact in float32; the sum is rounded to float32, then to the output type
+      T ko[8], vo[8];
+      const float ks = int4_scale(km[x]), kz = int4_zero(km[x]), vs = int4_scale(vm[x]), vz = int4_zero(vm[x]);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        ko[y] = Elem<T>::from_f(fmaf((float)(kc[x] >> (4 * y) & 15u), ks, kz));
+        vo[y] = Elem<T>::from_f(fmaf((float)(vc[x] >> (4 * y) & 15u), vs, vz));
+      }
+      const size_t o = ((size_t)(t0 + r) * c.Hkv + h) * D + 8 * l;
+      __stcs(reinterpret_cast<uint4*>(static_cast<T*>(a.k_out) + o), *reinterpret_cast<uint4*>(ko));
+      __stcs(reinterpret_cast<uint4*>(static_cast<T*>(a.v_out) + o), *reinterpret_cast<uint4*>(vo));
+    }
   }
 }
 
@@ -186,6 +255,10 @@ __global__ void __launch_bounds__(kRowThreads) int4_read_kernel(Int4View c, RowA
 // ---------------------------------------------------------------------------------------
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;                 // 11, 11 and 10 bits of the key
+constexpr int kSelKeys = 48 * 1024;            // keys a CTA holds in shared memory
+constexpr int kSelCtas = 8;                    // a portable cluster
 
 // Order of the entries: the newest ones above all, then by weight. A NaN weight is below every
 // other; -0 equals +0.
@@ -197,99 +270,182 @@ __device__ __forceinline__ uint32_t evict_key(float w, bool newest) {
   return (b >> 31) ? ~b : (b | 0x80000000u);
 }
 
-// The survivors of one unit, a CTA each: the budget-th highest key T by a radix select, the entries
-// above it, and of those equal to it the first ones. Their indices go, in order, to the pos slots
-// of their new places (the move kernel puts the positions there).
-__global__ void __launch_bounds__(kSelThreads) int4_select_kernel(Int4View s, Int4View d, int budget, int recent) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t ctl[2];
-  __shared__ int wsum[2][32];
-  __shared__ int base[2];
-  const int u = blockIdx.x, b = u / s.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// shared-memory word of another CTA of the cluster
+__device__ __forceinline__ uint32_t ld_peer(const void* p, int rank) {
+  uint32_t addr, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+struct SelShared {
+  uint32_t hist[2][kSelBins];
+  uint32_t sums[kSelWarps];
+  int wave[2][kSelWarps];       // per warp: entries equal to and above the threshold
+  int count[2];                 // of this CTA
+  uint32_t digit, above;
+  uint32_t keys[1];             // [this CTA's entries], when they fit
+};
+
+// The survivors of one unit, by a cluster of CTAs that hold consecutive parts of its entries: the
+// budget-th highest key T by a radix select whose histograms meet in distributed shared memory, the
+// entries above T, and of those equal to it the first ones. Their indices go, in order, to the pos
+// slots of their new places (the move kernel puts the positions there). The keys are read from global
+// memory once and kept in shared memory as far as they fit.
+__global__ void __launch_bounds__(kSelThreads) int4_select_kernel(Int4View s, Int4View d, int budget, int recent,
+                                                                  int ctas, int cap) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SelShared& sh = *reinterpret_cast<SelShared*>(smem_raw);
+  const int u = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  const int b = u / s.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t* table = s.table + (size_t)u * s.max_pages;
   const int32_t* dtable = d.table + (size_t)u * d.max_pages;
-  int len = s.lengths[u];
-  if (tid == 0 && u % s.Hkv == 0) d.seen[b] = s.seen[b];
-  if (len < 0 || (long long)len > (long long)s.max_pages * kInt4Page) {
-    if (tid == 0) {
+  const int len = s.lengths[u];
+  if (tid == 0 && rank == 0 && u % s.Hkv == 0) d.seen[b] = s.seen[b];
+  if (len < 0 || (long long)len > (long long)s.max_pages * kInt4Page) {   // alike in the whole cluster
+    if (tid == 0 && rank == 0) {
       qe_record_error(s.status, QE_ERR_INVALID_ARG, u);
       d.lengths[u] = 0;
     }
     return;
   }
+  // this CTA's entries: whole pages, so that a page's weights and positions are one wide load
+  const int pages = (len + kInt4Page - 1) / kInt4Page;
+  const int p0 = (int)((long long)pages * rank / ctas), p1 = (int)((long long)pages * (rank + 1) / ctas);
+  const int e0 = p0 * kInt4Page, mine = max(0, min(len, p1 * kInt4Page) - e0);
   const long long cut = (long long)s.seen[b] - recent;
-  auto key_of = [&](int e) -> uint32_t {
-    const int page = table[e / kInt4Page];
+  const bool held = mine <= cap, all = len <= budget;
+  auto global_key = [&](int x) -> uint32_t {       // of this CTA's entry x
+    const int page = table[p0 + x / kInt4Page];
     if (page < 0 || page >= s.n_pages) return 0u;
-    const size_t at = (size_t)page * kInt4Page + e % kInt4Page;
+    const size_t at = (size_t)page * kInt4Page + x % kInt4Page;
     return evict_key(s.mass[at], s.pos[at] >= cut);
   };
-  const int keep = min(len, budget);
-  uint32_t T = 0;         // keys above T are kept,
-  int ties = len;         // and the first `ties` equal to it
-  if (len > budget) {
+  auto key_of = [&](int x) { return held ? sh.keys[x] : global_key(x); };
+  uint32_t T = 0;           // keys above T are kept,
+  int ties = len;           // and the first `ties` equal to it
+  if (!all) {
+    for (int x = tid; x < kSelBins; x += kSelThreads) sh.hist[0][x] = sh.hist[1][x] = 0;
+    __syncthreads();
+    // quarter pages: four entries a thread, all look-ups of a round in flight together
+    for (int q = tid; q < (p1 - p0) * 4; q += kSelThreads) {
+      const int page = table[p0 + q / 4];
+      const bool ok = page >= 0 && page < s.n_pages;
+      const size_t at = (size_t)(ok ? page : 0) * kInt4Page + (q % 4) * 4;
+      const float4 w = *reinterpret_cast<const float4*>(s.mass + at);
+      const int4 p = *reinterpret_cast<const int4*>(s.pos + at);
+      const uint32_t k[4] = {evict_key(w.x, p.x >= cut), evict_key(w.y, p.y >= cut), evict_key(w.z, p.z >= cut),
+                             evict_key(w.w, p.w >= cut)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int x = q * 4 + j;
+        if (x >= mine) continue;
+        const uint32_t key = ok ? k[j] : 0u;
+        if (held) sh.keys[x] = key;
+        atomicAdd(&sh.hist[0][key >> 21], 1u);
+      }
+    }
     uint32_t prefix = 0, mask = 0;
     int k = budget;
-    for (int sh = 24; sh >= 0; sh -= 8) {
-      for (int x = tid; x < 256; x += kSelThreads) hist[x] = 0;
-      __syncthreads();
-      for (int e = tid; e < len; e += kSelThreads) {
-        const uint32_t key = key_of(e);
-        if ((key & mask) == prefix) atomicAdd(&hist[key >> sh & 255u], 1u);
+    for (int pass = 0; pass < 3; ++pass) {
+      const int sft = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t bins = pass == 2 ? 1024u : 2048u;
+      uint32_t* hist = sh.hist[pass & 1];
+      if (pass > 0)
+        for (int x = tid; x < mine; x += kSelThreads) {
+          const uint32_t key = key_of(x);
+          if ((key & mask) == prefix) atomicAdd(&hist[key >> sft & (bins - 1)], 1u);
+        }
+      if (ctas > 1) cluster_sync(); else __syncthreads();
+      // thread i owns bins 2i, 2i + 1, the highest first
+      const int hi = kSelBins - 1 - 2 * tid, lo = hi - 1;
+      uint32_t c_hi = 0, c_lo = 0;
+      if (ctas > 1) {
+#pragma unroll 1
+        for (int r = 0; r < ctas; ++r) c_hi += ld_peer(&hist[hi], r), c_lo += ld_peer(&hist[lo], r);
+      } else {
+        c_hi = hist[hi], c_lo = hist[lo];
       }
-      __syncthreads();
-      if (tid == 0) {
-        int above = 0, x = 255;
-        while (above + (int)hist[x] < k) above += hist[x--];
-        ctl[0] = x;
-        ctl[1] = above;
+      uint32_t inc = c_hi + c_lo;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
       }
+      if (lane == 31) sh.sums[warp] = inc;
       __syncthreads();
-      prefix |= ctl[0] << sh;
-      mask |= 255u << sh;
-      k -= ctl[1];
+      uint32_t before = sh.sums[lane];
+      uint32_t run = before;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      before = __shfl_sync(0xffffffffu, run - before, warp);
+      const uint32_t above_hi = before + inc - c_hi - c_lo, above_lo = above_hi + c_hi, want = (uint32_t)k;
+      if (above_hi < want && above_hi + c_hi >= want) sh.digit = hi, sh.above = above_hi;
+      if (above_lo < want && above_lo + c_lo >= want) sh.digit = lo, sh.above = above_lo;
+      // before the histogram that the next pass but one fills is cleared, every CTA has read it
+      if (ctas > 1) cluster_sync(); else __syncthreads();
+      if (pass == 0)
+        for (int x = tid; x < kSelBins; x += kSelThreads) hist[x] = 0;
+      prefix |= sh.digit << sft;
+      mask |= (bins - 1) << sft;
+      k -= (int)sh.above;
       __syncthreads();
     }
     T = prefix;
     ties = k;
   }
-  if (tid < 2) base[tid] = 0;
+  // order: each warp counts its consecutive entries, then writes them behind those before it
+  const int per = ((mine + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int w0 = min(mine, warp * per), w1 = min(mine, w0 + per);
+  int neq = 0, ngt = 0;
+  for (int x0 = w0; x0 < w1; x0 += 32) {
+    const int x = x0 + lane;
+    const uint32_t key = all ? 0u : x < w1 ? key_of(x) : 0u;
+    neq += __popc(__ballot_sync(0xffffffffu, x < w1 && (all || key == T)));
+    ngt += __popc(__ballot_sync(0xffffffffu, x < w1 && !all && key > T));
+  }
+  if (lane == 0) sh.wave[0][warp] = neq, sh.wave[1][warp] = ngt;
   __syncthreads();
-  for (int e0 = 0; e0 < len; e0 += kSelThreads) {
-    const int e = e0 + tid;
-    const uint32_t key = e < len ? key_of(e) : 0u;
-    const bool eq = e < len && (len <= budget || key == T), gt = e < len && len > budget && key > T;
-    const uint32_t beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
-    if (lane == 0) wsum[0][warp] = __popc(beq), wsum[1][warp] = __popc(bgt);
-    __syncthreads();
-    if (warp == 0) {
+  if (warp < 2) {
+    const int own = sh.wave[warp][lane];
+    int inc = own;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int own = wsum[w][lane];
-        int inc = own;
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        wsum[w][lane] = base[w] + inc - own;
-        __syncwarp();
-        if (lane == 31) base[w] += inc;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    __syncthreads();
-    const uint32_t below = (1u << lane) - 1u;
-    const int neq = wsum[0][warp] + __popc(beq & below), ngt = wsum[1][warp] + __popc(bgt & below);
-    if (gt || (eq && neq < ties)) {
-      const int to = ngt + min(neq, ties);
+    sh.wave[warp][lane] = inc - own;
+    if (lane == 31) sh.count[warp] = inc;
+  }
+  if (ctas > 1) cluster_sync(); else __syncthreads();
+  neq = sh.wave[0][warp], ngt = sh.wave[1][warp];
+  for (int r = 0; r < rank; ++r) neq += (int)ld_peer(&sh.count[0], r), ngt += (int)ld_peer(&sh.count[1], r);
+  const uint32_t below = (1u << lane) - 1u;
+  for (int x0 = w0; x0 < w1; x0 += 32) {
+    const int x = x0 + lane;
+    const uint32_t key = all ? 0u : x < w1 ? key_of(x) : 0u;
+    const bool eq = x < w1 && (all || key == T), gt = x < w1 && !all && key > T;
+    const uint32_t beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
+    const int at_eq = neq + __popc(beq & below), at_gt = ngt + __popc(bgt & below);
+    if (gt || (eq && at_eq < ties)) {
+      const int to = at_gt + min(at_eq, ties);
       const int page = dtable[to / kInt4Page];
       if (page < 0 || page >= d.n_pages)
         qe_record_error(d.status, QE_ERR_DEVICE_FAULT, u);
       else
-        d.pos[(size_t)page * kInt4Page + to % kInt4Page] = e;
+        d.pos[(size_t)page * kInt4Page + to % kInt4Page] = e0 + x;
     }
-    __syncthreads();
+    neq += __popc(beq);
+    ngt += __popc(bgt);
   }
-  if (tid == 0) d.lengths[u] = keep;
+  if (tid == 0 && rank == 0) d.lengths[u] = min(len, budget);
+  if (ctas > 1) cluster_sync();            // no CTA leaves while another reads its counts
 }
 
 // One warp assembles one destination page: the records of its entries, their weights and positions.
@@ -351,6 +507,14 @@ __global__ void __launch_bounds__(128) int4_move_kernel(Int4View s, Int4View d, 
   }
 }
 
+// a tile of rows of one head a warp, at most sixteen CTAs an SM
+int row_grid(int T, int Hkv, int D, int sms) {
+  const int tile = 8 * (128 / D);
+  const long long warps = ((long long)T + tile - 1) / tile * Hkv, per = kRowThreads / 32;
+  const long long want = (warps + per - 1) / per;
+  return (int)(want < 16ll * sms ? want : 16ll * sms);
+}
+
 int sm_count(int* sms) {
   static QeOnce once;
   static int of[QE_MAX_DEVICES];
@@ -368,7 +532,8 @@ int sm_count(int* sms) {
 int int4_view(const qe_int4_cache* c, Int4View* v) {
   if (!c || !c->pages || !c->page_table || !c->lengths || !c->seen || !c->mass || !c->pos || !c->status)
     return QE_ERR_INVALID_ARG;
-  if (c->B < 1 || c->Hkv < 1 || c->max_pages < 1 || c->n_pages < 1 || !qe_aligned(c->pages, 16))
+  if (c->B < 1 || c->Hkv < 1 || c->max_pages < 1 || c->n_pages < 1 || !qe_aligned(c->pages, 16) ||
+      !qe_aligned(c->mass, 16) || !qe_aligned(c->pos, 16))
     return QE_ERR_INVALID_ARG;
   if (c->D != 64 && c->D != 128) return QE_ERR_UNSUPPORTED_SHAPE;
   if ((long long)c->B * c->Hkv * c->max_pages * kInt4Page >= (1ll << 31)) return QE_ERR_UNSUPPORTED_SHAPE;
@@ -393,8 +558,7 @@ QE_API int qe_int4_append(const qe_int4_cache* cache, const void* k, const void*
   if ((e = sm_count(&sms))) return e;
   RowArgs a{};
   a.k = k, a.v = v, a.ks = k_stride, a.vs = v_stride, a.cu = cu_seqlens, a.mass = mass, a.T = T;
-  const long long per = kRowThreads / (D / 4), want = ((long long)T * c.Hkv + per - 1) / per;
-  const int grid = (int)(want < 8ll * sms ? want : 8ll * sms);
+  const int grid = row_grid(T, c.Hkv, D, sms);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = dtype == QE_BF16;
   if (D == 128) {
@@ -414,14 +578,13 @@ QE_API int qe_int4_read(const qe_int4_cache* cache, const int32_t* cu_seqlens, i
   if (e) return e;
   if (T < 0 || !cu_seqlens || (dtype != QE_FP16 && dtype != QE_BF16)) return QE_ERR_INVALID_ARG;
   if (T == 0) return QE_OK;
-  if (!k_out || !v_out || !qe_aligned(k_out, 8) || !qe_aligned(v_out, 8)) return QE_ERR_INVALID_ARG;
+  if (!k_out || !v_out || !qe_aligned(k_out, 16) || !qe_aligned(v_out, 16)) return QE_ERR_INVALID_ARG;
   int sms = 0;
   if ((e = sm_count(&sms))) return e;
   const int D = cache->D;
   RowArgs a{};
   a.k_out = k_out, a.v_out = v_out, a.cu = cu_seqlens, a.first = first, a.T = T;
-  const long long per = kRowThreads / (D / 4), want = ((long long)T * c.Hkv + per - 1) / per;
-  const int grid = (int)(want < 8ll * sms ? want : 8ll * sms);
+  const int grid = row_grid(T, c.Hkv, D, sms);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = dtype == QE_BF16;
   if (D == 128) {
@@ -444,8 +607,37 @@ QE_API int qe_int4_evict(const qe_int4_cache* src, const qe_int4_cache* dst, int
   if (s.pages == d.pages || s.lengths == d.lengths || s.seen == d.seen || s.mass == d.mass || s.pos == d.pos)
     return QE_ERR_INVALID_ARG;
   const int U = s.B * s.Hkv, ppu = (budget + kInt4Page - 1) / kInt4Page;
+  int sms = 0;
+  if ((e = sm_count(&sms))) return e;
+  static QeOnce once;
+  int dev = 0;
+  constexpr int kMaxSmem = (int)sizeof(SelShared) + kSelKeys * 4;
+  e = qe_once_per_device(once, &dev, [&](int) {
+    QE_CUDA_TRY(cudaFuncSetAttribute(int4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem));
+    return QE_OK;
+  });
+  if (e) return e;
+  // More CTAs a unit while its entries would not fit one's shared memory, or while SMs would stay
+  // idle and a CTA would still have 4096 entries or more (below that, meeting costs more than it saves)
+  const long long room = (long long)s.max_pages * kInt4Page;
+  int ctas = 1;
+  while (ctas < kSelCtas && (room > (long long)ctas * kSelKeys ||
+                             ((long long)U * ctas * 2 <= sms && room >= ctas * 2 * 4096ll)))
+    ctas *= 2;
+  const long long share = (s.max_pages + ctas - 1ll) / ctas * kInt4Page;
+  const int cap = (int)(share < kSelKeys ? share : kSelKeys);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  int4_select_kernel<<<U, kSelThreads, 0, st>>>(s, d, budget, recent);
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3(U * ctas);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = sizeof(SelShared) + (size_t)cap * 4;
+  cfg.stream = st;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)ctas, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, int4_select_kernel, s, d, budget, recent, ctas, cap) != cudaSuccess) return QE_ERR_CUDA;
   const int grid = (int)(((long long)U * ppu + 3) / 4);
   if (src->D == 128) int4_move_kernel<128><<<grid, 128, 0, st>>>(s, d, ppu);
   else int4_move_kernel<64><<<grid, 128, 0, st>>>(s, d, ppu);

@@ -14,30 +14,59 @@
 #include "qe_internal.cuh"
 
 constexpr int kInt4Page = 16;
+constexpr int kInt4Tickets = 4;   // words of the status array before the attention's tickets
 
-// Scale and zero of a group from its exact minimum and maximum: s = fp16(f32(f32(max - min) / 15)),
-// z = fp16(min), and the code of an element: clamp(rint(f32(f32(x - z) / s)), 0, 15), 0 if s == 0,
-// ties to even. The quotient is first taken with an approximate reciprocal (error below 15 x 2^-22);
-// within 1e-3 of a half-integer the correctly rounded division decides, so the code is that of the
-// definition in every case.
-struct Int4Group {
-  __half sh, zh;
-  float s, z, rs;
-  __device__ __forceinline__ Int4Group(float mn, float mx) {
-    sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
-    zh = __float2half_rn(mn);
-    s = __half2float(sh);
-    z = __half2float(zh);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
-    if (s == 0.f) rs = 0.f;
+// Scale and zero of a group from its exact minimum and maximum: s = fp16(f32(f32(max - min) / 15)), z =
+// fp16(min). The quotient is the correctly rounded one: q0 = RN(d RN(1/15)), corrected once by its
+// exact remainder (Markstein's division by a known constant; equal to IEEE division for every
+// float32 significand, and what underflows is 0 in fp16 either way).
+__device__ __forceinline__ uint32_t int4_meta(float mn, float mx) {
+  const float d = __fsub_rn(mx, mn), r15 = 0.0666666701436042785644531f;   // RN(1/15)
+  float q = __fmul_rn(d, r15);
+  q = isinf(d) ? d : __fmaf_rn(__fmaf_rn(-15.f, q, d), r15, q);
+  return static_cast<uint32_t>(__half_as_ushort(__float2half_rn(q))) |
+         (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(mn))) << 16);
+}
+__device__ __forceinline__ float int4_scale(uint32_t meta) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(meta & 0xffffu)));
+}
+__device__ __forceinline__ float int4_zero(uint32_t meta) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(meta >> 16)));
+}
+// 1 / (15 s), to about 2^-22; 0 for s == 0
+__device__ __forceinline__ float int4_inv15(uint32_t meta) {
+  const float s = int4_scale(meta);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s * 15.f));
+  return s == 0.f ? 0.f : r;
+}
+
+// Codes of four elements, nibble by nibble: clamp(rint(f32(f32(x - z) / s)), 0, 15), 0 if s == 0, ties
+// to even. y = (x - z) / (15 s) saturated to [0, 1] (the clamp's bounds are integers, so it may
+// come first) times 15 is the quotient to 15 x 2^-20; adding 1.5 x 2^23 rounds it into the sum's low
+// bits. When one of the four lies within 2^-12 of a half-integer the correctly rounded division
+// decides, so the codes are those of the definition in every case.
+__device__ __forceinline__ uint32_t int4_codes(float a, float b, float c, float d, uint32_t meta, float inv15) {
+  constexpr float kMagic = 12582912.f;   // 1.5 x 2^23: bits 0x4B400000
+  const float z = int4_zero(meta), x[4] = {a, b, c, d};
+  float far = 0.f;
+  uint32_t n = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float y = __saturatef(__fmul_rn(__fsub_rn(x[i], z), inv15));   // NaN gives 0
+    const float t = __fmaf_rn(y, 15.f, kMagic);
+    far = fmaxf(far, fabsf(__fmaf_rn(y, 15.f, __fsub_rn(kMagic, t))));
+    n += __float_as_uint(t) << (4 * i);   // the constant's low 16 bits are 0
   }
-  __device__ __forceinline__ uint32_t code(float x) const {
-    const float d = __fsub_rn(x, z);
-    float q = __fmul_rn(d, rs);
-    if (fabsf(q - rintf(q)) > 0.499f) q = __fdiv_rn(d, s);
-    return min(__float2uint_rn(q), 15u);   // negative values and NaN convert to 0
+  n &= 0xffffu;
+  if (far > 0.5f - 0x1p-12f) {
+    const float s = int4_scale(meta);
+    n = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n |= min(__float2uint_rn(__fdiv_rn(__fsub_rn(x[i], z), s)), 15u) << (4 * i);
   }
-};
+  return n;
+}
 
 // device view of a qe_int4_cache
 struct Int4View {
@@ -47,7 +76,7 @@ struct Int4View {
   int32_t* seen;       // [B]
   float* mass;         // [n_pages][16]
   int32_t* pos;        // [n_pages][16]
-  int32_t* status;     // [4]: code, detail, append's ticket, -
+  int32_t* status;     // code, detail, append's ticket, -, then attend's tickets
   int B, Hkv, max_pages, n_pages;
 };
 

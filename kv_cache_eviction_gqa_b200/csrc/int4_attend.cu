@@ -14,12 +14,12 @@
 // 16, times s once more): 2^-11 relative, below the output's own rounding in bf16 and equal to it
 // in fp16; their sums, the maxima and the scores are float32.
 //
-// Split: the pages of all units form one flat list, cut into equal ranges, one a CTA, so batches of
-// very different lengths load every SM alike. Warp w of a CTA takes every 4th page of a range,
-// each page one bulk copy into the warp's own ring. A range may cross units: per (CTA, unit) piece
-// the warps merge in shared memory and leave one partial (m, l, O). The scores of a weighing call go
-// to scratch (float32, mostly L2) and the second kernel turns them into weights once the unit's
-// maximum and sum are known.
+// Split: the pages of all units, each unit led by the weight of starting it, form one flat list that is
+// cut into equal ranges, one a CTA, so batches of very different lengths load every SM alike. Warp w of a CTA takes every 4th pair of pages of
+// a range, each page one bulk copy into the warp's own ring. A range may cross units: per (CTA, unit) piece
+// the warps merge in shared memory and leave one partial (m, l, O); the last CTA of a unit to arrive joins
+// its partials, always in the same order. The scores of a weighing call go to scratch (float32, mostly
+// L2) and a second kernel turns them into weights once the unit's maximum and sum are known.
 #include <math.h>
 
 #include "int4.cuh"
@@ -28,10 +28,23 @@
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStages = 4;
-constexpr int kCtasPerSm = 4;
-constexpr int kMinPages = 8;        // pages of a range below which more CTAs only add merging
-constexpr int kCombinePages = 64;   // pages of a unit that a CTA of the second kernel weighs
+constexpr int kPair = 2;            // pages of a step: two independent chains hide each other's latency
+constexpr int kStages = 3;
+constexpr int kCtasPerSm = 3;
+// one resident wave: a CTA more would only wait for another's end
+constexpr int kMaxCtas = 148 * kCtasPerSm;
+// below every score in the log2 domain
+constexpr float kLowest = -1e30f;
+constexpr int kJoin = 32;           // partials that one join takes: a lane each
+constexpr int kGroup = 16;
+static_assert(kMaxCtas / kGroup + 2 <= kJoin, "the groups of one unit fit a join");
+constexpr int kMinPages = 8;        // weight of a range below which more CTAs only add merging
+// A unit weighs its pages and this many more, about what starting and merging a piece costs: without
+// it a CTA that drew a run of short units ended last by far (16 000 to 1 tokens a sequence, 64 units:
+// 65 us, 46 of them such a CTA's)
+constexpr int kUnitWeight = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kWeighThreads = 256;  // of the second kernel, a quarter page each
 
 struct AttendArgs {
   Int4View c;
@@ -41,10 +54,15 @@ struct AttendArgs {
   int Hq, G, GP, weigh; // GP: G rounded up to a pair
   float cs;             // log2(e) / sqrt(D)
   int max_ctas;
-  int32_t* prefix;      // [U + 1] pages before each unit, then the number of CTAs that took part
+  int32_t* prefix;      // [U] places before each unit on the flat list
+  float* unit_ml;       // [U][2][8] maximum, 1 / sum
   float* part_ml;       // [slots][2][8]
   float* part_o;        // [slots][8][D]
-  float* scores;        // [flat pages][16][GP], log2 domain
+  float* group_ml;      // the same for groups of kGroup CTAs
+  float* group_o;
+  int32_t* tickets;     // [U] arrivals at a unit, 0 between calls
+  int32_t* group_tickets;   // [U + kMaxCtas / kGroup]
+  float* scores;        // [places][16][GP], log2 domain
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -90,109 +108,165 @@ __device__ __forceinline__ int unit_pages(const Int4View& c, int u) {
   return (len + kInt4Page - 1) / kInt4Page;
 }
 
-// first flat page of CTA c's range: floor(c P / C)
-__device__ __forceinline__ int range_at(int c, int P, int C) { return (int)((long long)c * P / C); }
-// the CTA whose range holds flat page p
-__device__ __forceinline__ int cta_of(int p, int P, int C) { return (int)((((long long)p + 1) * C - 1) / P); }
-__device__ __forceinline__ int ctas_for(int P, int most) {
-  const int c = (P + kMinPages - 1) / kMinPages;
+__device__ __forceinline__ int unit_weight(const Int4View& c, int u) {
+  const int n = unit_pages(c, u);
+  return n ? n + kUnitWeight : 0;
+}
+
+// first place of CTA c's range on the flat list of W places: floor(c W / C)
+__device__ __forceinline__ int range_at(int c, int W, int C) { return (int)((long long)c * W / C); }
+// the CTA whose range holds place p
+__device__ __forceinline__ int cta_of(int p, int W, int C) { return (int)((((long long)p + 1) * C - 1) / W); }
+__device__ __forceinline__ int ctas_for(int W, int most) {
+  const int c = (W + kMinPages - 1) / kMinPages;
   return c < most ? c : most;
 }
 
 template <int D>
 struct AttendLayout {
   static constexpr int PAGE = 20 * D;
-  static constexpr int RING = kStages * PAGE;            // a warp's; also holds its O for the merge
+  static constexpr int STAGE = kPair * PAGE;
+  static constexpr int RING = kStages * STAGE;           // a warp's; also holds its O for the merge
   static constexpr int SMEM = kWarps * RING + kWarps * kStages * 8;
   static_assert(RING >= 8 * D * 4, "a warp's partial output fits its ring");
 };
+
+// Joins n <= kJoin partials, a head's maxima and sums side by side in a warp's lanes: puts the joint
+// maximum and sum of each head into s_ml and hands out the joint outputs (relative to that maximum).
+template <int D, typename F>
+__device__ __forceinline__ void join_parts(const float* ml, const float* po, int n, int G, float (*s_f)[kJoin],
+                                           float (*s_ml)[8], F&& put) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int h = warp; h < G; h += kWarps) {
+    const float m = lane < n ? __ldcg(ml + lane * 16 + h) : kLowest;
+    float l = lane < n ? __ldcg(ml + lane * 16 + 8 + h) : 0.f, M = m;
+#pragma unroll
+    for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    const float f = ex2f(m - M);
+    l *= f;
+#pragma unroll
+    for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    s_f[h][lane] = f;
+    if (lane == 0) s_ml[0][h] = M, s_ml[1][h] = l;
+  }
+  __syncthreads();
+  for (int x = tid; x < G * D; x += kThreads) {
+    float acc = 0.f;
+    int y = 0;
+    for (; y + 8 <= n; y += 8) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __ldcg(po + (size_t)(y + j) * 8 * D + x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc = fmaf(v[j], s_f[x / D][y + j], acc);
+    }
+    float v[7];
+#pragma unroll
+    for (int j = 0; j < 7; ++j) v[j] = y + j < n ? __ldcg(po + (size_t)(y + j) * 8 * D + x) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (y + j < n) acc = fmaf(v[j], s_f[x / D][y + j], acc);
+    put(x, acc);
+  }
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(AttendArgs a) {
   using L = AttendLayout<D>;
   constexpr int NG = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_total, s_unit, s_base;
+  __shared__ int s_sum[kWarps], s_unit, s_base, s_last;
   __shared__ float s_m[kWarps][8], s_l[kWarps][8], s_z[kWarps][8][NG];
+  __shared__ float s_f[8][kJoin], s_ml[2][8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
   const Int4View& c = a.c;
-  const int U = c.B * c.Hkv;
+  const int U = c.B * c.Hkv, cta = blockIdx.x;
   uint8_t* ring = smem + warp * L::RING;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * L::RING) + warp * kStages;
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
   }
-  // ---- this CTA's range of the flat page list ----
-  if (warp == 0) {
-    int total = 0;
-    for (int u0 = 0; u0 < U; u0 += 32) {
-      const int n = u0 + lane < U ? unit_pages(c, u0 + lane) : 0;
-      int inc = n;
+  // ---- this CTA's range of the flat list: each thread weighs consecutive units ----
+  const int per = (U + kThreads - 1) / kThreads, u0 = min(U, tid * per), u1 = min(U, u0 + per);
+  int own = 0;
+  for (int x = u0; x < u1; ++x) own += unit_weight(c, x);
+  int inc = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (blockIdx.x == 0 && u0 + lane < U) a.prefix[u0 + lane] = total + inc - n;
-      total += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    const int C = ctas_for(total, a.max_ctas);
-    if (blockIdx.x == 0 && lane == 0) a.prefix[U] = total;
-    if (lane == 0) s_total = total;
-    if ((int)blockIdx.x < C) {           // the unit that holds the range's first page
-      const int p = range_at(blockIdx.x, total, C);
-      int before = 0;
-      for (int u0 = 0; u0 < U; u0 += 32) {
-        const int n = u0 + lane < U ? unit_pages(c, u0 + lane) : 0;
-        int inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, before + inc > p);
-        if (past) {
-          const int w = __ffs(past) - 1;
-          if (lane == w) s_unit = u0 + w, s_base = before + inc - n;
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, inc, 31);
-      }
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
   }
+  if (lane == 31) s_sum[warp] = inc;
   __syncthreads();
-  const int P = s_total, C = ctas_for(P, a.max_ctas), cta = blockIdx.x;
-  if (cta >= C) return;
-  const int p_end = range_at(cta + 1, P, C);
-  int p = range_at(cta, P, C), u = s_unit, base = s_base;
+  int P = 0, before = inc - own;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    P += s_sum[w];
+  }
+  const int C = ctas_for(P, a.max_ctas);
+  int p = cta < C ? range_at(cta, P, C) : P;
+  const int p_end = cta < C ? range_at(cta + 1, P, C) : P;
+  if (own && p >= before && p < before + own) {      // the unit that holds the range's first place
+    int x = u0, at = before;
+    for (int n = unit_weight(c, x); p >= at + n; n = unit_weight(c, x)) at += n, ++x;
+    s_unit = x, s_base = at;
+  }
+  if (cta == 0)
+    for (int x = u0, at = before; x < u1; ++x) {
+      const int n = unit_weight(c, x);
+      a.prefix[x] = at;
+      at += n;
+      if (n == 0) {                                  // no entries: the output is 0
+        T* dst = static_cast<T*>(a.out) + ((size_t)(x / c.Hkv) * a.Hq + (x % c.Hkv) * a.G) * D;
+        for (int y = 0; y < a.G * D; ++y) dst[y] = Elem<T>::from_f(0.f);
+      }
+    }
+  __syncthreads();
+  if (p >= p_end) return;
+  int u = s_unit, base = s_base;         // base: the place of the unit's first page
   uint32_t fills = 0;                    // copies this warp has waited for: stage and phase
   bool ok = true;
+  int np = unit_pages(c, u);
+  base += kUnitWeight;
 
-  while (p < p_end) {
-    // ---- one piece: pages p .. p1 - 1 of unit u ----
-    int np = unit_pages(c, u);
-    while (np == 0 || p >= base + np) {  // skip empty units
-      base += np;
-      np = unit_pages(c, ++u);
+  while (true) {
+    // ---- one piece: places p .. p1 - 1, pages p - base .. of unit u ----
+    while (p >= base + np) {             // the next unit that has entries
+      do np = unit_pages(c, ++u); while (np == 0 && p < p_end && u + 1 < U);
+      base = p + kUnitWeight;
     }
+    p = max(p, base);
+    if (p >= p_end) break;
     const int p1 = min(p_end, base + np), len = c.lengths[u];
     const int b = u / c.Hkv, kvh = u % c.Hkv;
-    const int32_t* table = c.table + (size_t)u * c.max_pages - base;
-    const int mine = (p1 - p - warp + kWarps - 1) / kWarps;   // this warp's pages: p + warp + kWarps i
-    auto issue = [&](int i) {
-      const int page = table[p + warp + kWarps * i];
-      const int s = (fills + i) % kStages;
-      if (page < 0 || page >= c.n_pages) {  // nothing is read: the page counts as masked
-        qe_record_error(c.status, QE_ERR_DEVICE_FAULT, u);
-        mbar_arrive_expect_tx(&bars[s], 0);
-        return;
-      }
-      mbar_arrive_expect_tx(&bars[s], L::PAGE);
-      bulk_g2s(ring + s * L::PAGE, c.pages + (size_t)page * L::PAGE, L::PAGE, &bars[s]);
+    const int32_t* table = c.table + (size_t)u * c.max_pages + (p - base);
+    // this warp's steps: pages p + 2 (warp + kWarps i) and the one behind it
+    const int mine = ((p1 - p + 1) / 2 - warp + kWarps - 1) / kWarps;
+    // Lane l holds the page of place l % 2 of the warp's step 16 x + l / 2, and of the next 16 steps, so
+    // that neither a copy nor a mask ever waits for the table. A page out of range, or behind the
+    // piece, becomes -1: nothing is read for it.
+    auto page_of = [&](int i) -> int {   // i = 2 step + place
+      const int at = 2 * (warp + kWarps * (i >> 1)) + (i & 1);
+      if (at >= p1 - p) return -1;
+      const int page = table[at];
+      if (page >= 0 && page < c.n_pages) return page;
+      qe_record_error(c.status, QE_ERR_DEVICE_FAULT, u);
+      return -1;
     };
-    if (lane == 0)
-      for (int i = 0; i < min(mine, kStages); ++i) issue(i);
+    int ids = page_of(lane), ids_next = page_of(32 + lane);
+    auto issue = [&](int i, int pa, int pb) {   // lane 0
+      const int s = (fills + i) % kStages;
+      mbar_arrive_expect_tx(&bars[s], ((pa >= 0) + (pb >= 0)) * L::PAGE);
+      if (pa >= 0) bulk_g2s(ring + s * L::STAGE, c.pages + (size_t)pa * L::PAGE, L::PAGE, &bars[s]);
+      if (pb >= 0) bulk_g2s(ring + s * L::STAGE + L::PAGE, c.pages + (size_t)pb * L::PAGE, L::PAGE, &bars[s]);
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {
+      const int pa = __shfl_sync(0xffffffffu, ids, 2 * i), pb = __shfl_sync(0xffffffffu, ids, 2 * i + 1);
+      if (lane == 0 && i < mine) issue(i, pa, pb);
+    }
 
     // ---- the queries: fp16 fragments scaled by 2^e, and their sums over groups ----
     uint32_t qf[2 * NG][2];
@@ -252,28 +326,40 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
         k2[j] = a.cs * __uint_as_float((uint32_t)(4 - eh + 127) << 23);
       }
     }
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // heads 2t, 2t + 1
+    // kLowest instead of -inf: below every score, and differences of it stay numbers
+    float m0 = kLowest, m1 = kLowest, l0 = 0.f, l1 = 0.f;   // heads 2t, 2t + 1
     float o[2 * NG][4], oz[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < 2 * NG; ++x)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[x][j] = 0.f;
+    const bool store = a.weigh && 2 * t < a.GP;
+    float* sc_out = a.scores + ((size_t)(p + 2 * warp) * kInt4Page + r) * a.GP + 2 * t;
+    int left = len - (p + 2 * warp - base) * kInt4Page;     // entries from this step's first on
+    int st = fills % kStages;
+    uint32_t ph = (fills / kStages) & 1;
 
     for (int i = 0; i < mine; ++i) {
-      const uint32_t f = fills + i;
-      const int s = f % kStages;
-      const int fp = p + warp + kWarps * i;
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&bars[s], (f / kStages) & 1, c.status, 6001));
+      if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[st], ph)))
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], ph, c.status, 6001));
       if (!ok) break;
-      const uint8_t* pg = ring + s * L::PAGE;
+      const uint8_t* pg = ring + st * L::STAGE;
+      const int i5 = (2 * i) & 31;
+      const int live[kPair] = {__shfl_sync(0xffffffffu, ids, i5) < 0 ? 0 : left,
+                               __shfl_sync(0xffffffffu, ids, i5 + 1) < 0 ? 0 : left - kInt4Page};
+      const bool whole = live[0] >= kInt4Page && live[1] >= kInt4Page;
       // ---- scores ----
-      float sc[4] = {0.f, 0.f, 0.f, 0.f}, sz[4] = {0.f, 0.f, 0.f, 0.f};
-      {
+      float sc[kPair][4];
+#pragma unroll
+      for (int y = 0; y < kPair; ++y) {
+        const uint8_t* py = pg + y * L::PAGE;
+        float sz[4] = {0.f, 0.f, 0.f, 0.f};
+        sc[y][0] = sc[y][1] = sc[y][2] = sc[y][3] = 0.f;
         uint32_t ka[2][NG], ks[2][NG / 2];
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-          const uint8_t* row = pg + (r + 8 * hr) * (D / 2) + t * (NG * 4);
-          const uint8_t* meta = pg + 16 * D + (r + 8 * hr) * (NG * 2);
+          const uint8_t* row = py + (r + 8 * hr) * (D / 2) + t * (NG * 4);
+          const uint8_t* meta = py + 16 * D + (r + 8 * hr) * (NG * 2);
           if (NG == 4) {
             const uint4 w = *reinterpret_cast<const uint4*>(row);
             ka[hr][0] = w.x, ka[hr][1] = w.y, ka[hr][NG - 2] = w.z, ka[hr][NG - 1] = w.w;
@@ -286,8 +372,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
           }
         }
         const int zo = NG == 4 ? (t & 1) * 4 : 0;
-        mma_k8(sz, *reinterpret_cast<const uint32_t*>(pg + 17 * D + r * (NG * 2) + zo),
-               *reinterpret_cast<const uint32_t*>(pg + 17 * D + (r + 8) * (NG * 2) + zo), qs);
+        mma_k8(sz, *reinterpret_cast<const uint32_t*>(py + 17 * D + r * (NG * 2) + zo),
+               *reinterpret_cast<const uint32_t*>(py + 17 * D + (r + 8) * (NG * 2) + zo), qs);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -297,26 +383,32 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
                   qf[2 * g + 1][1]);
           const float s0 = g & 1 ? h_hi(ks[0][g / 2]) : h_lo(ks[0][g / 2]);
           const float s1 = g & 1 ? h_hi(ks[1][g / 2]) : h_lo(ks[1][g / 2]);
-          sc[0] = fmaf(acc[0], s0, sc[0]), sc[1] = fmaf(acc[1], s0, sc[1]);
-          sc[2] = fmaf(acc[2], s1, sc[2]), sc[3] = fmaf(acc[3], s1, sc[3]);
+          sc[y][0] = fmaf(acc[0], s0, sc[y][0]), sc[y][1] = fmaf(acc[1], s0, sc[y][1]);
+          sc[y][2] = fmaf(acc[2], s1, sc[y][2]), sc[y][3] = fmaf(acc[3], s1, sc[y][3]);
         }
-        sc[0] = fmaf(sc[0], k1[0], sz[0] * k2[0]), sc[1] = fmaf(sc[1], k1[1], sz[1] * k2[1]);
-        sc[2] = fmaf(sc[2], k1[0], sz[2] * k2[0]), sc[3] = fmaf(sc[3], k1[1], sz[3] * k2[1]);
+        sc[y][0] = fmaf(sc[y][0], k1[0], sz[0] * k2[0]), sc[y][1] = fmaf(sc[y][1], k1[1], sz[1] * k2[1]);
+        sc[y][2] = fmaf(sc[y][2], k1[0], sz[2] * k2[0]), sc[y][3] = fmaf(sc[y][3], k1[1], sz[3] * k2[1]);
       }
-      // entries of this page inside the unit; none when its table entry was out of range
-      const int pgid = table[fp];
-      const int live = pgid < 0 || pgid >= c.n_pages ? 0 : min(kInt4Page, len - (fp - base) * kInt4Page);
-      if (live < kInt4Page) {
-        if (r >= live) sc[0] = sc[1] = -INFINITY;
-        if (r + 8 >= live) sc[2] = sc[3] = -INFINITY;
+      if (!whole) {                      // entries behind the unit's last, or of an absent page
+#pragma unroll
+        for (int y = 0; y < kPair; ++y) {
+          if (r >= live[y]) sc[y][0] = sc[y][1] = -INFINITY;
+          if (r + 8 >= live[y]) sc[y][2] = sc[y][3] = -INFINITY;
+        }
       }
-      if (a.weigh && 2 * t < a.GP) {
-        float* dst = a.scores + ((size_t)fp * kInt4Page + r) * a.GP + 2 * t;
-        *reinterpret_cast<float2*>(dst) = make_float2(sc[0], sc[1]);
-        *reinterpret_cast<float2*>(dst + 8 * a.GP) = make_float2(sc[2], sc[3]);
+      if (store) {
+        *reinterpret_cast<float2*>(sc_out) = make_float2(sc[0][0], sc[0][1]);
+        *reinterpret_cast<float2*>(sc_out + 8 * a.GP) = make_float2(sc[0][2], sc[0][3]);
+        if (whole || live[1] > 0) {      // the place behind an odd last page may be another CTA's
+          *reinterpret_cast<float2*>(sc_out + 16 * a.GP) = make_float2(sc[1][0], sc[1][1]);
+          *reinterpret_cast<float2*>(sc_out + 24 * a.GP) = make_float2(sc[1][2], sc[1][3]);
+        }
       }
+      sc_out += 2 * kWarps * kInt4Page * a.GP;
+      left -= 2 * kWarps * kInt4Page;
       // ---- softmax: the maxima move rarely, and then all lanes of a head together ----
-      const float x0 = fmaxf(sc[0], sc[2]), x1 = fmaxf(sc[1], sc[3]);
+      const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
+      const float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
       if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
         float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
 #pragma unroll
@@ -324,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
           n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, w));
           n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, w));
         }
-        const float f0 = m0 == n0 ? 1.f : ex2f(m0 - n0), f1 = m1 == n1 ? 1.f : ex2f(m1 - n1);
+        const float f0 = ex2f(m0 - n0), f1 = ex2f(m1 - n1);
         m0 = n0, m1 = n1;
         l0 *= f0, l1 *= f1;
 #pragma unroll
@@ -332,51 +424,69 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
         oz[0] *= f0, oz[1] *= f1;
       }
       // 16 p: the factor cancels in the output and keeps p s clear of fp16's subnormals
-      const float b0f = m0 == -INFINITY ? 0.f : m0 - 4.f, b1f = m1 == -INFINITY ? 0.f : m1 - 4.f;
-      const float p00 = ex2f(sc[0] - b0f), p01 = ex2f(sc[1] - b1f), p10 = ex2f(sc[2] - b0f), p11 = ex2f(sc[3] - b1f);
-      l0 += p00 + p10, l1 += p01 + p11;
-      const uint32_t pb0 = movm_t(pack_h2(p00, p01)), pb1 = movm_t(pack_h2(p10, p11));
-      // ---- output: rows are elements, the contraction runs over the 16 entries ----
-      uint32_t vs[NG][2], vz[2];
+      const float b0 = m0 - 4.f, b1 = m1 - 4.f;
+      uint32_t pb[kPair][2];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint2 w = *reinterpret_cast<const uint2*>(pg + 18 * D + (t * NG + g) * 8);
-        vs[g][0] = w.x, vs[g][1] = w.y;
+      for (int y = 0; y < kPair; ++y) {
+        const float p00 = ex2f(sc[y][0] - b0), p01 = ex2f(sc[y][1] - b1);
+        const float p10 = ex2f(sc[y][2] - b0), p11 = ex2f(sc[y][3] - b1);
+        l0 += p00 + p10, l1 += p01 + p11;
+        pb[y][0] = movm_t(pack_h2(p00, p01)), pb[y][1] = movm_t(pack_h2(p10, p11));
       }
-      {
-        const uint2 w = *reinterpret_cast<const uint2*>(pg + 19 * D + (t * NG + (r & (NG - 1))) * 8);
-        vz[0] = r < NG ? w.x : 0u, vz[1] = r < NG ? w.y : 0u;
-      }
-      if (live < kInt4Page) {            // what dead slots hold may be anything: 0 x NaN is not 0
-        auto keep = [&](int i0) { return (i0 < live ? 0xffffu : 0u) | (i0 + 1 < live ? 0xffff0000u : 0u); };
-        const uint32_t k_lo = keep(2 * t), k_hi = keep(2 * t + 8);
+      // ---- output: rows are elements, the contraction runs over a page's 16 entries ----
 #pragma unroll
-        for (int g = 0; g < NG; ++g) vs[g][0] &= k_lo, vs[g][1] &= k_hi;
-        vz[0] &= k_lo, vz[1] &= k_hi;
-      }
-      mma_k16(oz, vz[0], 0u, vz[1], 0u, pb0, pb1);
-      uint32_t va[4][NG / 2];            // entries 2t, 2t + 1, 2t + 8, 2t + 9
+      for (int y = 0; y < kPair; ++y) {
+        const uint8_t* py = pg + y * L::PAGE;
+        uint32_t vs[NG][2], vz[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* row = pg + 8 * D + (2 * t + (j & 1) + 8 * (j >> 1)) * (D / 2) + r * (NG * 2);
-        if (NG == 4) {
-          const uint2 w = *reinterpret_cast<const uint2*>(row);
-          va[j][0] = w.x, va[j][NG / 2 - 1] = w.y;
-        } else {
-          va[j][0] = *reinterpret_cast<const uint32_t*>(row);
+        for (int g = 0; g < NG; g += 2) {
+          const uint4 w = *reinterpret_cast<const uint4*>(py + 18 * D + (t * NG + g) * 8);
+          vs[g][0] = w.x, vs[g][1] = w.y, vs[g + 1][0] = w.z, vs[g + 1][1] = w.w;
+        }
+        {
+          const uint2 w = *reinterpret_cast<const uint2*>(py + 19 * D + (t * NG + (r & (NG - 1))) * 8);
+          vz[0] = r < NG ? w.x : 0u, vz[1] = r < NG ? w.y : 0u;
+        }
+        if (!whole) {                    // what dead slots hold may be anything: 0 x NaN is not 0
+          auto keep = [&](int i0) { return (i0 < live[y] ? 0xffffu : 0u) | (i0 + 1 < live[y] ? 0xffff0000u : 0u); };
+          const uint32_t k_lo = keep(2 * t), k_hi = keep(2 * t + 8);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) vs[g][0] &= k_lo, vs[g][1] &= k_hi;
+          vz[0] &= k_lo, vz[1] &= k_hi;
+        }
+        mma_k16(oz, vz[0], 0u, vz[1], 0u, pb[y][0], pb[y][1]);
+        uint32_t va[4][NG / 2];          // entries 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint8_t* row = py + 8 * D + (2 * t + (j & 1) + 8 * (j >> 1)) * (D / 2) + r * (NG * 2);
+          if (NG == 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(row);
+            va[j][0] = w.x, va[j][NG / 2 - 1] = w.y;
+          } else {
+            va[j][0] = *reinterpret_cast<const uint32_t*>(row);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+          const uint32_t lo = __byte_perm(va[0][g / 2], va[1][g / 2], sel), hi = __byte_perm(va[2][g / 2], va[3][g / 2], sel);
+          const uint32_t q0 = hmul2(pb[y][0], vs[g][0]), q1 = hmul2(pb[y][1], vs[g][1]);
+          mma_k16(o[2 * g], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, q0, q1);
+          mma_k16(o[2 * g + 1], (lo >> 8) & 0x000f000fu, (lo >> 8) & 0x00f000f0u, (hi >> 8) & 0x000f000fu,
+                  (hi >> 8) & 0x00f000f0u, q0, q1);
         }
       }
-      __syncwarp();
-      if (lane == 0 && i + kStages < mine) issue(i + kStages);   // every lane has read the page
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-        const uint32_t lo = __byte_perm(va[0][g / 2], va[1][g / 2], sel), hi = __byte_perm(va[2][g / 2], va[3][g / 2], sel);
-        const uint32_t q0 = hmul2(pb0, vs[g][0]), q1 = hmul2(pb1, vs[g][1]);
-        mma_k16(o[2 * g], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, q0, q1);
-        mma_k16(o[2 * g + 1], (lo >> 8) & 0x000f000fu, (lo >> 8) & 0x00f000f0u, (hi >> 8) & 0x000f000fu,
-                (hi >> 8) & 0x00f000f0u, q0, q1);
+      {                                  // every lane has read the pages: their stage takes the next ones
+        const int n = 2 * (i + kStages);
+        const int from = (n ^ (2 * i)) & 32 ? ids_next : ids;
+        const int pa = __shfl_sync(0xffffffffu, from, n & 31), pb2 = __shfl_sync(0xffffffffu, from, (n & 31) + 1);
+        if (lane == 0 && i + kStages < mine) issue(i + kStages, pa, pb2);
+        if (i5 == 30) {
+          ids = ids_next;
+          ids_next = page_of(2 * i + 34 + lane);
+        }
       }
+      if (++st == kStages) st = 0, ph ^= 1;
     }
     fills += mine > 0 ? mine : 0;
     if (!ok) break;                      // the status word holds the reason
@@ -399,98 +509,133 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
         *reinterpret_cast<float4*>(wo + (2 * t + j) * D + 32 * g + 4 * r) =
             make_float4(o[2 * g][j] * kLo, o[2 * g][j + 2] * kHi, o[2 * g + 1][j] * kLo, o[2 * g + 1][j + 2] * kHi);
     __syncthreads();
-    {
-      const size_t slot = (size_t)cta + u;
-      for (int x = tid; x < a.G * D; x += kWarps * 32) {
-        const int h = x / D, d = x % D;
-        float M = -INFINITY;
+    const int c0 = cta_of(base, P, C), c1 = cta_of(base + np - 1, P, C);   // the unit's CTAs
+    const size_t slot = (size_t)cta + u;   // distinct: from piece to piece either grows
+    T* dst = static_cast<T*>(a.out) + ((size_t)b * a.Hq + kvh * a.G) * D;
+    for (int x = tid; x < a.G * D; x += kThreads) {
+      const int h = x / D, d = x % D;
+      float M = kLowest;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
-        float acc = 0.f, l = 0.f;
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][h]);
+      float acc = 0.f, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = s_m[w][h] == -INFINITY ? 0.f : ex2f(s_m[w][h] - M);
-          acc = fmaf(f, reinterpret_cast<const float*>(smem + w * L::RING)[h * D + d] + s_z[w][h][d / 32], acc);
-          l = fmaf(f, s_l[w][h], l);
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2f(s_m[w][h] - M);
+        acc = fmaf(f, reinterpret_cast<const float*>(smem + w * L::RING)[h * D + d] + s_z[w][h][d / 32], acc);
+        l = fmaf(f, s_l[w][h], l);
+      }
+      const float il = l > 0.f ? 1.f / l : 0.f;
+      if (c0 == c1) {                      // the whole unit
+        dst[x] = Elem<T>::from_f(acc * il);
+        if (d == 0) a.unit_ml[u * 16 + h] = M, a.unit_ml[u * 16 + 8 + h] = il;
+      } else {
         a.part_o[slot * 8 * D + x] = acc;
         if (d == 0) a.part_ml[slot * 16 + h] = M, a.part_ml[slot * 16 + 8 + h] = l;
+      }
+    }
+    if (c0 != c1) {
+      // whether this CTA is the last of n to arrive at a ticket; its partial is visible by then
+      auto last_of = [&](int32_t* ticket, int n) -> bool {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          s_last = atomicAdd(ticket, 1) == n - 1;
+          if (s_last) *ticket = 0;
+        }
+        __syncthreads();
+        if (s_last) __threadfence();
+        return s_last;
+      };
+      float* ml = a.part_ml + ((size_t)c0 + u) * 16;
+      float* po = a.part_o + ((size_t)c0 + u) * 8 * D;
+      int n = c1 - c0 + 1;
+      bool join = true;
+      if (n > kJoin) {                     // a long unit of a small batch: groups of kGroup CTAs first
+        const int g = cta / kGroup, ga = max(c0, g * kGroup), gb = min(c1, g * kGroup + kGroup - 1);
+        float* gml = a.group_ml + ((size_t)g + u) * 16;
+        float* gpo = a.group_o + ((size_t)g + u) * 8 * D;
+        join = last_of(a.group_tickets + g + u, gb - ga + 1);
+        if (join)
+          join_parts<D>(ml + (ga - c0) * 16, po + (size_t)(ga - c0) * 8 * D, gb - ga + 1, a.G, s_f, s_ml,
+                        [&](int x, float acc) { gpo[x] = acc; });
+        if (join && tid < a.G) gml[tid] = s_ml[0][tid], gml[8 + tid] = s_ml[1][tid];
+        ml = a.group_ml + ((size_t)(c0 / kGroup) + u) * 16;
+        po = a.group_o + ((size_t)(c0 / kGroup) + u) * 8 * D;
+        n = c1 / kGroup - c0 / kGroup + 1;
+      }
+      if (join && last_of(a.tickets + u, n)) {
+        join_parts<D>(ml, po, n, a.G, s_f, s_ml, [&](int x, float acc) {
+          const float l = s_ml[1][x / D];
+          dst[x] = Elem<T>::from_f(l > 0.f ? acc / l : 0.f);
+        });
+        if (tid < a.G) {
+          const float l = s_ml[1][tid];
+          a.unit_ml[u * 16 + tid] = s_ml[0][tid], a.unit_ml[u * 16 + 8 + tid] = l > 0.f ? 1.f / l : 0.f;
+        }
       }
     }
     fence_proxy_async_smem();            // the rings take bulk copies again
     __syncthreads();
     p = p1;
+    if (p >= p_end) break;
   }
 }
 
-// Joins a unit's partials: chunk 0 writes the output, and every chunk adds its entries' weights.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) int4_combine_kernel(AttendArgs a) {
-  __shared__ float s_M[8], s_il[8];
+// The weights of a unit's entries from their scores: four entries, a quarter page, a thread. Launched
+// behind the kernel above without waiting for it to drain; it waits here. Bound by the scores' way
+// through L2 and the weights' through HBM.
+__global__ void __launch_bounds__(kWeighThreads) int4_weigh_kernel(AttendArgs a) {
   const Int4View& c = a.c;
-  const int U = c.B * c.Hkv, u = blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x;
-  const int base = a.prefix[u], P = a.prefix[U], np = a.prefix[u + 1] - base;
-  const int b = u / c.Hkv, kvh = u % c.Hkv;
-  if (chunk * kCombinePages >= np) {
-    if (chunk == 0) {                    // no entries: the output is 0
-      T* dst = static_cast<T*>(a.out) + ((size_t)b * a.Hq + kvh * a.G) * D;
-      for (int x = tid; x < a.G * D; x += 128) dst[x] = Elem<T>::from_f(0.f);
-    }
-    return;
-  }
-  const int C = ctas_for(P, a.max_ctas);
-  const int c0 = cta_of(base, P, C), c1 = cta_of(base + np - 1, P, C);
-  if (tid < a.G) {
-    float M = -INFINITY, l = 0.f;
-    for (int x = c0; x <= c1; ++x) M = fmaxf(M, a.part_ml[((size_t)x + u) * 16 + tid]);
-    for (int x = c0; x <= c1; ++x) {
-      const float m = a.part_ml[((size_t)x + u) * 16 + tid];
-      if (m != -INFINITY) l = fmaf(a.part_ml[((size_t)x + u) * 16 + 8 + tid], ex2f(m - M), l);
-    }
-    s_M[tid] = M;
-    s_il[tid] = l > 0.f ? 1.f / l : 0.f;
-  }
-  __syncthreads();
-  if (chunk == 0) {
-    T* dst = static_cast<T*>(a.out) + ((size_t)b * a.Hq + kvh * a.G) * D;
-    for (int x = tid; x < a.G * D; x += 128) {
-      const int h = x / D;
-      float acc = 0.f;
-      for (int y = c0; y <= c1; ++y) {
-        const float m = a.part_ml[((size_t)y + u) * 16 + h];
-        if (m != -INFINITY) acc = fmaf(a.part_o[((size_t)y + u) * 8 * D + x], ex2f(m - s_M[h]), acc);
-      }
-      dst[x] = Elem<T>::from_f(acc * s_il[h]);
-    }
-  }
-  if (!a.weigh) return;
+  const int u = blockIdx.y, q = blockIdx.x * kWeighThreads + threadIdx.x, e = q * 4;
   const int len = c.lengths[u];
-  const int e1 = min(len, (chunk + 1) * kCombinePages * kInt4Page);
-  for (int e = chunk * kCombinePages * kInt4Page + tid; e < e1; e += 128) {
-    const int page = c.table[(size_t)u * c.max_pages + e / kInt4Page];
-    if (page < 0 || page >= c.n_pages) continue;   // recorded by the first kernel
-    const float* sc = a.scores + ((size_t)base * kInt4Page + e) * a.GP;
-    float w = 0.f;
-    for (int h = 0; h < a.G; ++h) w += ex2f(sc[h] - s_M[h] + 4.f) * s_il[h];
-    c.mass[(size_t)page * kInt4Page + e % kInt4Page] += w;
+  const bool live = len >= 0 && (long long)len <= (long long)c.max_pages * kInt4Page && e < len;
+  const int page = live ? c.table[(size_t)u * c.max_pages + q / 4] : -1;
+  const bool has = page >= 0 && page < c.n_pages;  // a bad one was recorded by the first kernel
+  float* m = c.mass + (has ? (size_t)page * kInt4Page + e % kInt4Page : 0);
+  const float4 was = has ? *reinterpret_cast<const float4*>(m) : make_float4(0.f, 0.f, 0.f, 0.f);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!has) return;
+  const float* ml = a.unit_ml + u * 16;
+  const float* sc = a.scores + ((size_t)(a.prefix[u] + kUnitWeight) * kInt4Page + e) * a.GP;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int h = 0; h < a.G; h += 2) {
+    float2 s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = __ldcs(reinterpret_cast<const float2*>(sc + j * a.GP + h));
+    const float m0 = ml[h] - 4.f, i0 = ml[8 + h];
+    const bool pair = h + 1 < a.G;
+    const float m1 = pair ? ml[h + 1] - 4.f : 0.f, i1 = pair ? ml[9 + h] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = fmaf(ex2f(s[j].x - m0), i0, w[j]);
+      if (pair) w[j] = fmaf(ex2f(s[j].y - m1), i1, w[j]);
+    }
+  }
+  if (e + 4 <= len) {
+    *reinterpret_cast<float4*>(m) = make_float4(was.x + w[0], was.y + w[1], was.z + w[2], was.w + w[3]);
+  } else {                                         // slots behind the last entry stay as they were
+    m[0] = was.x + w[0];
+    if (e + 1 < len) m[1] = was.y + w[1];
+    if (e + 2 < len) m[2] = was.z + w[2];
   }
 }
 
 struct ScratchLayout {
-  size_t prefix, part_ml, part_o, scores, bytes;
+  size_t prefix, unit_ml, part_ml, part_o, group_ml, group_o, scores, bytes;
   ScratchLayout(long long units, int G, int D, long long max_pages, int ctas) {
     auto r = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t slots = (size_t)ctas + units;
     prefix = 0;
-    part_ml = r((units + 1) * 4);
+    unit_ml = r(units * 4);
+    part_ml = unit_ml + r(units * 16 * 4);
     part_o = part_ml + r(slots * 16 * 4);
-    scores = part_o + r(slots * 8 * D * 4);
-    bytes = scores + r((size_t)units * max_pages * kInt4Page * ((G + 1) & ~1) * 4);
+    const size_t groups = (size_t)ctas / kGroup + 1 + units;
+    group_ml = part_o + r(slots * 8 * D * 4);
+    group_o = group_ml + r(groups * 16 * 4);
+    scores = group_o + r(groups * 8 * D * 4);
+    bytes = scores + r((size_t)units * (max_pages + kUnitWeight) * kInt4Page * ((G + 1) & ~1) * 4);
   }
 };
-
-// One resident wave, whatever the device: a CTA more would only wait for another's end.
-constexpr int kMaxCtas = 148 * kCtasPerSm;
 
 template <typename T, int D>
 int launch(const AttendArgs& a, cudaStream_t st) {
@@ -504,10 +649,20 @@ int launch(const AttendArgs& a, cudaStream_t st) {
   });
   if (e) return e;
   const int U = a.c.B * a.c.Hkv;
-  const long long most = ((long long)U * a.c.max_pages + kMinPages - 1) / kMinPages;
+  const long long most = ((long long)U * (a.c.max_pages + kUnitWeight) + kMinPages - 1) / kMinPages;
   kern<<<(int)(most < a.max_ctas ? most : a.max_ctas), kWarps * 32, L::SMEM, st>>>(a);
-  const int chunks = a.weigh ? (a.c.max_pages + kCombinePages - 1) / kCombinePages : 1;
-  int4_combine_kernel<T, D><<<dim3(chunks, U), 128, 0, st>>>(a);
+  if (a.weigh) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3((a.c.max_pages * 4 + kWeighThreads - 1) / kWeighThreads, U);
+    cfg.blockDim = dim3(kWeighThreads);
+    cfg.stream = st;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, int4_weigh_kernel, a) != cudaSuccess) return QE_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? QE_OK : QE_ERR_CUDA;
 }
 
@@ -543,8 +698,13 @@ QE_API int qe_int4_attend(const qe_int4_cache* cache, const void* q, long long q
   a.cs = 1.4426950408889634f / sqrtf((float)D);
   a.max_ctas = kMaxCtas;
   a.prefix = reinterpret_cast<int32_t*>(w + S.prefix);
+  a.unit_ml = reinterpret_cast<float*>(w + S.unit_ml);
   a.part_ml = reinterpret_cast<float*>(w + S.part_ml);
   a.part_o = reinterpret_cast<float*>(w + S.part_o);
+  a.group_ml = reinterpret_cast<float*>(w + S.group_ml);
+  a.group_o = reinterpret_cast<float*>(w + S.group_o);
+  a.tickets = a.c.status + kInt4Tickets;
+  a.group_tickets = a.tickets + a.c.B * a.c.Hkv;
   a.scores = reinterpret_cast<float*>(w + S.scores);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (D == 128)

@@ -524,9 +524,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                  : 0.f;
     };
     float next = t < two ? fetch(0) : 0.f;
-    float2 acc = make_float2(0.f, 0.f);
+    // A key of a long prompt adds up a hundred thousand weights: each tile's 128 are summed apart and
+    // join the total with their rounding carried along (one plain float32 sum was off by 2e-5 of the
+    // whole at 16 000 positions, this one by the scores' own error).
+    float total = 0.f, carry = 0.f;
     for (int i = 0; t < two && i < N; ++i) {
       const int b = i & 1;
+      float2 acc = make_float2(0.f, 0.f);
       gL[b * kTileM + gr] = next;
       if (i + 1 < N) next = fetch(i + 1);
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
@@ -563,8 +567,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sfree[2 * t + b]);
+      const float y = __fsub_rn(__fadd_rn(acc.x, acc.y), carry), sum = __fadd_rn(total, y);
+      carry = __fsub_rn(__fsub_rn(sum, total), y);
+      total = sum;
     }
-    if (t < two && key < len) a.mass[(size_t)(start + key) * a.Hkv + kvh] = acc.x + acc.y;
+    if (t < two && key < len) a.mass[(size_t)(start + key) * a.Hkv + kvh] = total;
   }
   tc_fence_before();
   __syncthreads();
