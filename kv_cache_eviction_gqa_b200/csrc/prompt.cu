@@ -22,7 +22,13 @@ constexpr int kTileM = 128;             // packed query rows, keys, and accumula
 constexpr int kBoxBytes = 128 * 128;    // 128 rows x 64 16-bit elements
 constexpr int kTmemAll = 512;
 constexpr int kRoleWarps = 8;           // two groups of four: one TMEM lane a thread, a tile a group
-constexpr int kPromptThreads = (kRoleWarps + 2) * 32;
+constexpr int kPromptThreads = (kRoleWarps + 4) * 32;   // and a group of four for copies and products
+// Registers after the split: two groups of 128 threads take 208, the third 80, together 63 488 of the
+// 168 x 384 = 64 512 that the block is launched with.
+constexpr int kRegsRow = 208, kRegsRest = 80;
+constexpr int kFirstK = 6;              // of the eight 16-key steps of P V, those that start early
+constexpr int kMassPolyOf = 3;          // of every 8 pairs of the weights' kernel
+constexpr int kPolyOf = 4;              // of every 16 exponential pairs, those taken by polynomial
 
 struct PromptArgs {
   const int32_t* cu;      // [B + 1]
@@ -39,6 +45,31 @@ __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 2^x of two arguments without the special-function unit, whose rate bounds both kernels: x = n + f with
+// n the nearest integer, taken by adding 1.5 x 2^23, and a polynomial of degree 5 in f in [-1/2, 1/2]
+// (least maximal relative error, fitted by iteratively reweighted least squares: 7.5e-8, 2.1e-7 evaluated in
+// float32; ex2.approx has 2e-7); n is added to the exponent. Arguments from -127 up to 8.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  constexpr float kMagic = 12582912.f;
+  x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
+  const float2 t = __fadd2_rn(x, make_float2(kMagic, kMagic));
+  const float2 f = __fadd2_rn(x, __fadd2_rn(make_float2(kMagic, kMagic), make_float2(-t.x, -t.y)));
+  float2 p = make_float2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
+  auto step = [&](float c) { p = __ffma2_rn(p, f, make_float2(c, c)); };
+  step(9.675540961325169e-3f);
+  step(5.550713092088699e-2f);
+  step(2.4022120237350464e-1f);
+  step(6.931469440460205e-1f);
+  step(1.0000001192092896f);
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -59,6 +90,17 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+  uint32_t addr;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 #define QE_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), \
                     "=r"(v[o + 6]), "=r"(v[o + 7])
 #define QE_W8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), \
@@ -71,11 +113,25 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* v) {
       : QE_R8(v, 0), QE_R8(v, 8), QE_R8(v, 16), QE_R8(v, 24)
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : QE_R8(v, 0), QE_R8(v, 8)
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
       "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::QE_W8(v, 0),
       QE_W8(v, 8), QE_W8(v, 16), QE_W8(v, 24), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15};" ::QE_W8(v, 0),
+      QE_W8(v, 8), "r"(taddr)
       : "memory");
 }
 #undef QE_R8
@@ -179,8 +235,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* full = qfull + 2;                                             // [NS]
   uint64_t* empty = full + S::NS;                                         // [NS]
   uint64_t* sfull = empty + S::NS;                                        // [2] scores in TMEM
-  uint64_t* pfull = sfull + 2;                                            // [2] weights in TMEM
-  uint64_t* odone = pfull + 2;                                            // [2] P V added
+  uint64_t* pfull = sfull + 2;                                            // [2][2] weights in TMEM: 96, 128 columns
+  uint64_t* odone = pfull + 4;                                            // [2] P V added
   uint64_t* vclean = odone + 2;                                           // foreign rows of the last V cleared
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vclean + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -196,7 +252,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[2 * i], 4);
+      mbar_init(&pfull[2 * i + 1], 4);
       mbar_init(&odone[i], 1);
     }
     for (int s = 0; s < S::NS; ++s) {
@@ -225,179 +282,210 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const bool dirty = N * kTileM > len;
   const int clears = nt[1] == N ? 1 : 0;   // the group that sees the last tile clears those rows
 
-  if (len > 0 && warp == 8) {
-    if (lane == 0) {
-      for (int t = 0; t < 2; ++t) {
-        if (nt[t] == 0) continue;
-        mbar_arrive_expect_tx(&qfull[t], S::KB * a.G * a.PT * 128);
-        for (int kb = 0; kb < S::KB; ++kb)
-          tma_load_3d(sQ + t * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + pos0 + t * a.PT, &qfull[t]);
-      }
-      for (int i = 0; i < 2 * N; ++i) {
-        const int s = i % S::NS;
-        if (!wait_or_abort(&empty[s], ((i / S::NS) & 1) ^ 1, abort_flag, a.status, 5001)) break;
-        mbar_arrive_expect_tx(&full[s], S::TILE);
-        const CUtensorMap* tm = (i & 1) ? &tmV : &tmK;
-        for (int kb = 0; kb < S::KB; ++kb)
-          tma_load_3d(sKV + s * S::TILE + kb * kBoxBytes, tm, kb * 64, kvh, start + (i >> 1) * kTileM, &full[s]);
-      }
-    }
-  } else if (len > 0 && warp == 9) {
-    if (lane == 0) {
-      auto wait_full = [&](int i) {
-        return wait_or_abort(&full[i % S::NS], (i / S::NS) & 1, abort_flag, a.status, 5002);
-      };
-      auto qk = [&](int t, int i) {       // S_t = Q_t K_i^T
-        const uint8_t* sK = sKV + ((2 * i) % S::NS) * S::TILE;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * kBoxBytes + (k % 4) * 32;
-          mma_f16(tmem + t * kTileM, sdesc(smem_u32(sQ + t * S::TILE + off), 16, 1024),
-                  sdesc(smem_u32(sK + off), 16, 1024), ID_QK, k > 0 ? 1u : 0u);
+  if (warp >= kRoleWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (len > 0 && warp == 8) {
+      if (lane == 0) {
+        for (int t = 0; t < 2; ++t) {
+          if (nt[t] == 0) continue;
+          mbar_arrive_expect_tx(&qfull[t], S::KB * a.G * a.PT * 128);
+          for (int kb = 0; kb < S::KB; ++kb)
+            tma_load_3d(sQ + t * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + pos0 + t * a.PT, &qfull[t]);
         }
-        mma_commit(&sfull[t]);
-      };
-      bool ok = wait_full(0);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (nt[t] == 0) continue;
-        ok = wait_or_abort(&qfull[t], 0, abort_flag, a.status, 5003);
-        tc_fence_after();
-        if (ok) qk(t, 0);
+        for (int i = 0; i < 2 * N; ++i) {
+          const int s = i % S::NS;
+          if (!wait_or_abort(&empty[s], ((i / S::NS) & 1) ^ 1, abort_flag, a.status, 5001)) break;
+          mbar_arrive_expect_tx(&full[s], S::TILE);
+          const CUtensorMap* tm = (i & 1) ? &tmV : &tmK;
+          for (int kb = 0; kb < S::KB; ++kb)
+            tma_load_3d(sKV + s * S::TILE + kb * kBoxBytes, tm, kb * 64, kvh, start + (i >> 1) * kTileM, &full[s]);
+        }
       }
-      if (ok && S::NS < 2 * N) mma_commit(&empty[0]);
-      for (int i = 0; i < N && ok; ++i) {
-        const int sv = (2 * i + 1) % S::NS;
-        ok = wait_full(2 * i + 1);
-        if (ok && i == N - 1 && dirty) ok = wait_or_abort(vclean, 0, abort_flag, a.status, 5004);
+    } else if (len > 0 && warp == 9) {
+      if (lane == 0) {
+        auto wait_full = [&](int i) {
+          return wait_or_abort(&full[i % S::NS], (i / S::NS) & 1, abort_flag, a.status, 5002);
+        };
+        auto qk = [&](int t, int i) {       // S_t = Q_t K_i^T
+          const uint8_t* sK = sKV + ((2 * i) % S::NS) * S::TILE;
+  #pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * kBoxBytes + (k % 4) * 32;
+            mma_f16(tmem + t * kTileM, sdesc(smem_u32(sQ + t * S::TILE + off), 16, 1024),
+                    sdesc(smem_u32(sK + off), 16, 1024), ID_QK, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&sfull[t]);
+        };
+        bool ok = wait_full(0);
         for (int t = 0; t < 2 && ok; ++t) {
-          if (i < nt[t]) {
-            ok = wait_or_abort(&pfull[t], i & 1, abort_flag, a.status, 5005);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kTileM / 16; ++k)
-              mma_f16_ts(tmem + 2 * kTileM + t * kTileM, tmem + t * kTileM + k * 8,
-                         sdesc(smem_u32(sKV + sv * S::TILE + k * 16 * 128), kBoxBytes, 1024), ID_PV,
-                         i > 0 || k > 0 ? 1u : 0u);
-            mma_commit(&odone[t]);
-          }
-          if (t == 1 && 2 * i + 1 + S::NS < 2 * N) mma_commit(&empty[sv]);
-          if (i + 1 < N) {
-            if (t == 0) ok = wait_full(2 * i + 2);
-            if (ok && i + 1 < nt[t]) qk(t, i + 1);
-            if (t == 1 && 2 * i + 2 + S::NS < 2 * N) mma_commit(&empty[(2 * i + 2) % S::NS]);
+          if (nt[t] == 0) continue;
+          ok = wait_or_abort(&qfull[t], 0, abort_flag, a.status, 5003);
+          tc_fence_after();
+          if (ok) qk(t, 0);
+        }
+        if (ok && S::NS < 2 * N) mma_commit(&empty[0]);
+        for (int i = 0; i < N && ok; ++i) {
+          const int sv = (2 * i + 1) % S::NS;
+          ok = wait_full(2 * i + 1);
+          if (ok && i == N - 1 && dirty) ok = wait_or_abort(vclean, 0, abort_flag, a.status, 5004);
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (i < nt[t]) {
+              ok = wait_or_abort(&pfull[2 * t], i & 1, abort_flag, a.status, 5005);
+              if (!ok) break;
+              tc_fence_after();
+  #pragma unroll
+              for (int k = 0; k < kTileM / 16; ++k) {
+                if (k == kFirstK) {
+                  ok = wait_or_abort(&pfull[2 * t + 1], i & 1, abort_flag, a.status, 5010);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                mma_f16_ts(tmem + 2 * kTileM + t * kTileM, tmem + t * kTileM + k * 8,
+                           sdesc(smem_u32(sKV + sv * S::TILE + k * 16 * 128), kBoxBytes, 1024), ID_PV,
+                           i > 0 || k > 0 ? 1u : 0u);
+              }
+              if (!ok) break;
+              mma_commit(&odone[t]);
+            }
+            if (t == 1 && 2 * i + 1 + S::NS < 2 * N) mma_commit(&empty[sv]);
+            if (i + 1 < N) {
+              if (t == 0) ok = wait_full(2 * i + 2);
+              if (ok && i + 1 < nt[t]) qk(t, i + 1);
+              if (t == 1 && 2 * i + 2 + S::NS < 2 * N) mma_commit(&empty[(2 * i + 2) % S::NS]);
+            }
           }
         }
       }
     }
-  } else if (len > 0) {
-    // ---- softmax ----
-    const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
-    const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
-    const uint32_t tS = lane_addr + t * kTileM, tO = lane_addr + 2 * kTileM + t * kTileM;
-    const int pos = pos0 + t * a.PT + r / a.G;
-    const int n = nt[t];
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    auto clear_foreign = [&]() {        // rows >= len of the last V tile
-      const int i = 2 * (N - 1) + 1;
-      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&full[i % S::NS], (i / S::NS) & 1, abort_flag, a.status, 5006));
-      if (!ok) return;
-      uint8_t* sV = sKV + (i % S::NS) * S::TILE;
-      const int row0 = len - (N - 1) * kTileM;
-      for (int x = row0 * 8 + r; x < kTileM * 8; x += kTileM)
-        for (int kb = 0; kb < S::KB; ++kb)
-          *reinterpret_cast<uint4*>(sV + kb * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(vclean);
-    };
-    for (int i = 0; i < n && ok; ++i) {
-      ok = __all_sync(0xffffffffu, wait_or_abort(&sfull[t], i & 1, abort_flag, a.status, 5007));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t v[kTileM];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) tmem_ld_x32(tS + 32 * j, v + 32 * j);
-      tmem_wait_ld();
-      const int lim = pos - i * kTileM;   // columns 0..lim are seen
-      if (i * kTileM + kTileM - 1 > pos0 + t * a.PT) {
-#pragma unroll
-        for (int j = 0; j < kTileM; ++j)
-          if (j > lim) v[j] = 0xff800000u;
-      }
-      float mx = m;
-#pragma unroll
-      for (int j = 0; j < kTileM; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
-      const bool up = (mx - m) * a.c > 8.f;          // true on the first tile (m = -inf)
-      const float mo = m;
-      if (up) m = mx;
-      if (i > 0 && __any_sync(0xffffffffu, up)) {
-        const float f = up ? ex2f((mo - m) * a.c) : 1.f;
-        l *= f;
-        ok = __all_sync(0xffffffffu, wait_or_abort(&odone[t], (i - 1) & 1, abort_flag, a.status, 5008));
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRow));
+    if (len > 0) {
+      // ---- softmax ----
+      const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
+      const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+      const uint32_t tS = lane_addr + t * kTileM, tO = lane_addr + 2 * kTileM + t * kTileM;
+      const int pos = pos0 + t * a.PT + r / a.G;
+      const int n = nt[t];
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      auto clear_foreign = [&]() {        // rows >= len of the last V tile
+        const int i = 2 * (N - 1) + 1;
+        if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&full[i % S::NS], (i / S::NS) & 1, abort_flag, a.status, 5006));
+        if (!ok) return;
+        uint8_t* sV = sKV + (i % S::NS) * S::TILE;
+        const int row0 = len - (N - 1) * kTileM;
+        for (int x = row0 * 8 + r; x < kTileM * 8; x += kTileM)
+          for (int kb = 0; kb < S::KB; ++kb)
+            *reinterpret_cast<uint4*>(sV + kb * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vclean);
+      };
+      for (int i = 0; i < n && ok; ++i) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&sfull[t], i & 1, abort_flag, a.status, 5007));
         if (!ok) break;
         tc_fence_after();
+        uint32_t v[kTileM];
+        const bool open = i * kTileM + kTileM - 1 <= pos0 + t * a.PT;   // every row sees every key
+        const int lim = pos - i * kTileM;   // columns 0..lim are seen
+        float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+        auto rows_max = [&](int j0) {       // of 64 columns, four chains
+          if (!open) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (j0 + j > lim) v[j0 + j] = 0xff800000u;
+          }
+#pragma unroll
+          for (int j = 0; j < 64; j += 2)
+            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(v[j0 + j]), __uint_as_float(v[j0 + j + 1]));
+        };
+        tmem_ld_x32(tS, v);
+        tmem_ld_x32(tS + 32, v + 32);
+        tmem_wait_ld();
+        tmem_ld_x32(tS + 64, v + 64);       // under way while the first half is searched
+        tmem_ld_x32(tS + 96, v + 96);
+        rows_max(0);
+        tmem_wait_ld();
+        rows_max(64);
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        const bool up = (top - m) * a.c > 8.f;         // true on the first tile (m = -inf)
+        const float mo = m;
+        if (up) m = top;
+        if (i > 0 && __any_sync(0xffffffffu, up)) {
+          const float f = up ? ex2f((mo - m) * a.c) : 1.f;
+          l *= f;
+          ok = __all_sync(0xffffffffu, wait_or_abort(&odone[t], (i - 1) & 1, abort_flag, a.status, 5008));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < D / 16; ++j) {
+            float o[16];
+            tmem_ld_x16(tO + 16 * j, reinterpret_cast<uint32_t*>(o));
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] *= f;
+            tmem_st_x16(tO + 16 * j, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+        const float2 c2 = make_float2(a.c, a.c), mc2 = make_float2(-m * a.c, -m * a.c);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // The weights are rounded once, to the type of V, for the product; their sum is not. kPolyOf of
+        // every 16 pairs go to the FMA pipes (not in masked tiles: 0 there comes out as 2^-127).
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+          for (int j = 32 * q4; j < 32 * q4 + 32; j += 2) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, mc2);
+            float2 e;
+            if ((j / 2) % 16 >= 16 - kPolyOf && open) e = ex2_poly(x);
+            else e = make_float2(ex2f(x.x), ex2f(x.y));
+            sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], e);
+            if (BF16)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[j / 2]) : "f"(e.y), "f"(e.x));
+            else
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[j / 2]) : "f"(e.y), "f"(e.x));
+          }
+          tmem_st_x16(tS + 16 * q4, v + 16 * q4);
+          if (q4 == kFirstK / 2 - 1 || q4 == 3) {      // the product starts on three quarters of the weights
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[2 * t + (q4 == 3)]);
+          }
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if (i == N - 1 && dirty && t == clears) clear_foreign();
+      }
+      if (n > 0 && ok)
+        ok = __all_sync(0xffffffffu, wait_or_abort(&odone[t], (n - 1) & 1, abort_flag, a.status, 5009));
+      if (n > 0 && ok) {
+        tc_fence_after();
+        const float inv = 1.f / l;
+        const bool mine = r < a.G * a.PT && pos < len;
+        const size_t row = (size_t)(start + pos) * a.Hq + kvh * a.G + r % a.G;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * 2);
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           uint32_t o[32];
           tmem_ld_x32(tO + 32 * j, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-          tmem_st_x32(tO + 32 * j, o);
+          for (int x = 0; x < 32; x += 2) {
+            const float lo = __uint_as_float(o[x]) * inv, hi = __uint_as_float(o[x + 1]) * inv;
+            if (BF16)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
+            else
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
+          }
+          if (mine) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              dst[j * 4 + x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
         }
+        if (mine && a.lse) a.lse[row] = (m * a.c + log2f(l)) * 0.693147180559945309f;
       }
-      const float mc = m * a.c;
-      float2 sum = make_float2(0.f, 0.f);
-      // the weights are rounded once, to the type of V, for the product; their sum is not
-#pragma unroll
-      for (int j = 0; j < kTileM; j += 2) {
-        const float x = ex2f(fmaf(__uint_as_float(v[j]), a.c, -mc));
-        const float y = ex2f(fmaf(__uint_as_float(v[j + 1]), a.c, -mc));
-        sum = __fadd2_rn(sum, make_float2(x, y));
-        if (BF16)
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[j / 2]) : "f"(y), "f"(x));
-        else
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[j / 2]) : "f"(y), "f"(x));
-      }
-      l += sum.x + sum.y;
-      tmem_st_x32(tS, v);
-      tmem_st_x32(tS + 32, v + 32);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[t]);
-      if (i == N - 1 && dirty && t == clears) clear_foreign();
-    }
-    if (n > 0 && ok)
-      ok = __all_sync(0xffffffffu, wait_or_abort(&odone[t], (n - 1) & 1, abort_flag, a.status, 5009));
-    if (n > 0 && ok) {
-      tc_fence_after();
-      const float inv = 1.f / l;
-      const bool mine = r < a.G * a.PT && pos < len;
-      const size_t row = (size_t)(start + pos) * a.Hq + kvh * a.G + r % a.G;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * 2);
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        uint32_t o[32];
-        tmem_ld_x32(tO + 32 * j, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const float lo = __uint_as_float(o[x]) * inv, hi = __uint_as_float(o[x + 1]) * inv;
-          if (BF16)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
-          else
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
-        }
-        if (mine) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            dst[j * 4 + x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-        }
-      }
-      if (mine && a.lse) a.lse[row] = (m * a.c + log2f(l)) * 0.693147180559945309f;
+  
     }
   }
   tc_fence_before();
@@ -416,19 +504,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 // them. The scores are taken with the keys as rows, S = K Q^T, so a thread owns a key and its sum
 // over queries never leaves its registers: mass = sum_r exp2(c s_r - log2(e) lse_r). Warp roles as
 // above; each group's scores go through two TMEM buffers (2 tiles x 2 x 128 columns), so the
-// products run ahead of the exponentials that bound this kernel.
+// products run ahead of the exponentials that bound this kernel. When there are too few keys to
+// fill the GPU, a cluster of CTAs owns the same keys, each taking every ranks-th query tile, and the
+// first one adds the sums up in the order of ranks.
 template <int D>
 struct MassSmem {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kBoxBytes;
   static constexpr int NS = 3;
   static constexpr int NB = 4;                       // lse rows in flight (a power of two)
-  static constexpr int BYTES = 1024 + (2 + NS) * TILE + NB * kTileM * 4 + 256;
+  static constexpr int BYTES = 1024 + (2 + NS) * TILE + (NB + 2) * kTileM * 4 + 256;
 };
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    prompt_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, PromptArgs a) {
+    prompt_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, PromptArgs a,
+                       int ranks) {
   using S = MassSmem<D>;
   constexpr uint32_t ID = idesc_f16(BF16, false, kTileM, kTileM);
   extern __shared__ uint8_t smem_raw[];
@@ -436,7 +527,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* sK = smem;
   uint8_t* sQ = smem + 2 * S::TILE;
   float* sL = reinterpret_cast<float*>(sQ + S::NS * S::TILE);             // [2][2][128]: per group, double
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(sL + S::NB * kTileM);
+  float* sSum = sL + S::NB * kTileM;                                      // [256] for the cluster's first CTA
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(sSum + 2 * kTileM);
   uint64_t* full = kfull + 1;                                             // [NS]
   uint64_t* empty = full + S::NS;                                         // [NS]
   uint64_t* sfull = empty + S::NS;                                        // [2 tiles][2]
@@ -446,9 +538,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   int* sTile = reinterpret_cast<int*>(tmem_slot + 2);                     // [3]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x % a.Hkv;
+  const int rank = blockIdx.x % ranks, item = blockIdx.x / ranks, kvh = item % a.Hkv;
   if (warp == 0) {
-    const TileRef t = find_tile(a, 2 * kTileM, blockIdx.x / a.Hkv, true);
+    const TileRef t = find_tile(a, 2 * kTileM, item / a.Hkv, true);
     if (lane == 0) sTile[0] = t.start, sTile[1] = t.len, sTile[2] = t.tile;
   }
   if (threadIdx.x == 32) {
@@ -471,8 +563,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int start = sTile[0], len = sTile[1], key0 = sTile[2] * 2 * kTileM;
   const int two = key0 + kTileM < len ? 2 : 1;           // key tiles inside the sequence
-  const int qt0 = key0 / a.PT, qt1 = (len + a.PT - 1) / a.PT;   // query tiles that see them
-  const int N = len > 0 ? qt1 - qt0 : 0;
+  // query tiles that see them: this CTA's are qt0, qt0 + ranks, ...
+  const int qt0 = key0 / a.PT + rank, qt1 = (len + a.PT - 1) / a.PT;
+  const int N = len > 0 && qt1 > qt0 ? (qt1 - qt0 + ranks - 1) / ranks : 0;
 
   if (N > 0 && warp == 8) {
     if (lane == 0) {
@@ -485,7 +578,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (!wait_or_abort(&empty[s], ((i / S::NS) & 1) ^ 1, abort_flag, a.status, 5101)) break;
         mbar_arrive_expect_tx(&full[s], S::KB * a.G * a.PT * 128);
         for (int kb = 0; kb < S::KB; ++kb)
-          tma_load_3d(sQ + s * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + (qt0 + i) * a.PT, &full[s]);
+          tma_load_3d(sQ + s * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + (qt0 + i * ranks) * a.PT, &full[s]);
       }
     }
   } else if (N > 0 && warp == 9) {
@@ -509,18 +602,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (i + S::NS < N) mma_commit(&empty[s]);
       }
     }
-  } else if (N > 0) {
+  } else if (N > 0 && warp < kRoleWarps) {
     const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
     const int key = key0 + t * kTileM + r;
     const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
     const int gr = threadIdx.x & 127;                    // the query row whose lse this thread fetches
     const int gp = gr / a.G, gh = gr % a.G;
-    float* gL = sL + t * 2 * kTileM;
+    float* gL = sL + t * 2 * kTileM;                     // -log2(e) lse, double-buffered
     const int rows = a.G * a.PT;
     auto fetch = [&](int i) -> float {
-      const int p = (qt0 + i) * a.PT + gp;
+      const int p = (qt0 + i * ranks) * a.PT + gp;
       return gr < rows && p < len
-                 ? a.lse_in[(size_t)(start + p) * a.Hq + kvh * a.G + gh] * 1.4426950408889634f
+                 ? a.lse_in[(size_t)(start + p) * a.Hq + kvh * a.G + gh] * -1.4426950408889634f
                  : 0.f;
     };
     float next = t < two ? fetch(0) : 0.f;
@@ -528,50 +621,73 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // join the total with their rounding carried along (one plain float32 sum was off by 2e-5 of the
     // whole at 16 000 positions, this one by the scores' own error).
     float total = 0.f, carry = 0.f;
+    const float2 c2 = make_float2(a.c, a.c);
     for (int i = 0; t < two && i < N; ++i) {
       const int b = i & 1;
-      float2 acc = make_float2(0.f, 0.f);
       gL[b * kTileM + gr] = next;
       if (i + 1 < N) next = fetch(i + 1);
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
       if (!__all_sync(0xffffffffu, wait_or_abort(&sfull[2 * t + b], (i >> 1) & 1, abort_flag, a.status, 5105))) break;
       tc_fence_after();
-      const int p0 = (qt0 + i) * a.PT;
+      const int p0 = (qt0 + i * ranks) * a.PT;
       const bool open = p0 >= key0 + (t + 1) * kTileM - 1 && p0 + a.PT <= len && rows == kTileM;
-      // the columns this key is seen by: first at or after it, last inside the sequence
-      const int c_lo = max(0, key - p0) * a.G, c_hi = min(rows, (len - p0) * a.G);
-#pragma unroll
-      for (int j = 0; j < kTileM; j += 32) {
-        uint32_t v[32];
-        tmem_ld_x32(lane_addr + (2 * t + b) * kTileM + j, v);
+      const uint32_t tS = lane_addr + (2 * t + b) * kTileM;
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      if (open) {
+        uint32_t v[2][32];
+        tmem_ld_x32(tS, v[0]);
         tmem_wait_ld();
-        const float4* bias = reinterpret_cast<const float4*>(gL + b * kTileM + j);
-        if (open) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < 3) tmem_ld_x32(tS + 32 * (j + 1), v[(j + 1) & 1]);   // under way during these
+          const float4* bias = reinterpret_cast<const float4*>(gL + b * kTileM + 32 * j);
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             const float4 w = bias[x / 4];
-            const float e0 = ex2f(fmaf(__uint_as_float(v[x]), a.c, -w.x));
-            const float e1 = ex2f(fmaf(__uint_as_float(v[x + 1]), a.c, -w.y));
-            const float e2 = ex2f(fmaf(__uint_as_float(v[x + 2]), a.c, -w.z));
-            const float e3 = ex2f(fmaf(__uint_as_float(v[x + 3]), a.c, -w.w));
-            acc = __fadd2_rn(acc, __fadd2_rn(make_float2(e0, e1), make_float2(e2, e3)));
+            const uint32_t* y = v[j & 1] + x;
+            const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), c2, make_float2(w.x, w.y));
+            const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), c2, make_float2(w.z, w.w));
+            const bool poly = (x / 4) % 4 >= 4 - kMassPolyOf;
+            acc[0] = __fadd2_rn(acc[0], make_float2(ex2f(x0.x), ex2f(x0.y)));
+            acc[1] = __fadd2_rn(acc[1], poly ? ex2_poly(x1) : make_float2(ex2f(x1.x), ex2f(x1.y)));
           }
-        } else {
+          if (j < 3) tmem_wait_ld();
+        }
+      } else {
+        // the columns this key is seen by: first at or after it, last inside the sequence
+        const int c_lo = max(0, key - p0) * a.G, c_hi = min(rows, (len - p0) * a.G);
+#pragma unroll 1
+        for (int j = 0; j < kTileM; j += 32) {
+          uint32_t v[32];
+          tmem_ld_x32(tS + j, v);
+          tmem_wait_ld();
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
-            const float e = ex2f(fmaf(__uint_as_float(v[x]), a.c, -gL[b * kTileM + j + x]));
-            if (j + x >= c_lo && j + x < c_hi) acc.x += e;
+            const float e = ex2f(fmaf(__uint_as_float(v[x]), a.c, gL[b * kTileM + j + x]));
+            if (j + x >= c_lo && j + x < c_hi) acc[x & 1].x += e;
           }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sfree[2 * t + b]);
-      const float y = __fsub_rn(__fadd_rn(acc.x, acc.y), carry), sum = __fadd_rn(total, y);
+      const float y = __fsub_rn((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y), carry), sum = __fadd_rn(total, y);
       carry = __fsub_rn(__fsub_rn(sum, total), y);
       total = sum;
     }
-    if (t < two && key < len) a.mass[(size_t)(start + key) * a.Hkv + kvh] = total;
+    if (ranks > 1) sSum[t * kTileM + r] = total;
+    else if (t < two && key < len) a.mass[(size_t)(start + key) * a.Hkv + kvh] = total;
+  }
+  if (ranks > 1) {
+    if (N == 0 && threadIdx.x < 2 * kTileM) sSum[threadIdx.x] = 0.f;
+    __syncwarp();
+    cluster_sync_all();
+    if (rank == 0 && len > 0 && threadIdx.x < 2 * kTileM && key0 + (int)threadIdx.x < len) {
+      float total = 0.f;
+      for (int r = 0; r < ranks; ++r) total += ld_cluster(sSum + threadIdx.x, r);
+      a.mass[(size_t)(start + key0 + threadIdx.x) * a.Hkv + kvh] = total;
+    }
+    cluster_sync_all();                  // no CTA leaves while its sums are read
   }
   tc_fence_before();
   __syncthreads();
@@ -641,8 +757,10 @@ int launch_mass(const void* q, const void* k, long long qs, long long ks, Prompt
   using S = MassSmem<D>;
   auto kern = prompt_mass_kernel<D, BF16>;
   static QeOnce once;
+  static int sms_of[QE_MAX_DEVICES];
   int dev = 0;
-  int e = qe_once_per_device(once, &dev, [&](int) {
+  int e = qe_once_per_device(once, &dev, [&](int d) {
+    QE_CUDA_TRY(cudaDeviceGetAttribute(&sms_of[d], cudaDevAttrMultiProcessorCount, d));
     QE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES));
     return QE_OK;
   });
@@ -650,8 +768,23 @@ int launch_mass(const void* q, const void* k, long long qs, long long ks, Prompt
   CUtensorMap tmQ, tmK;
   if ((e = make_map3(&tmQ, q, BF16, D, a.Hq, a.T, qs, a.G, a.PT))) return e;
   if ((e = make_map3(&tmK, k, BF16, D, a.Hkv, a.T, ks, 1, kTileM))) return e;
-  const int tiles = a.T / (2 * kTileM) + (a.B < a.T ? a.B : a.T);
-  kern<<<tiles * a.Hkv, kPromptThreads, S::BYTES, st>>>(tmQ, tmK, a);
+  const int items = (a.T / (2 * kTileM) + (a.B < a.T ? a.B : a.T)) * a.Hkv;
+  // Two items an SM and more balance by themselves, longest first. Below that the longest alone would
+  // decide: 8192 positions, 2 kv heads of 8: 949 us with one CTA for a tile of keys, the products of a
+  // 148th of the work being 110
+  int ranks = 1;
+  while (ranks < 8 && items * ranks < 2 * sms_of[dev]) ranks *= 2;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3((unsigned)items * ranks);
+  cfg.blockDim = dim3(kPromptThreads);
+  cfg.dynamicSmemBytes = S::BYTES;
+  cfg.stream = st;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)ranks, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, a, ranks) != cudaSuccess) return QE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QE_OK : QE_ERR_CUDA;
 }
 
