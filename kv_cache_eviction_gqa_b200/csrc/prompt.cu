@@ -12,6 +12,8 @@
 // box (64 elements, G heads, PT tokens) brings such a tile in, whatever the token stride.
 #include <math.h>
 
+#include <type_traits>
+
 #include "tc_common.cuh"
 
 namespace {
@@ -23,12 +25,14 @@ constexpr int kBoxBytes = 128 * 128;    // 128 rows x 64 16-bit elements
 constexpr int kTmemAll = 512;
 constexpr int kRoleWarps = 8;           // two groups of four: one TMEM lane a thread, a tile a group
 constexpr int kPromptThreads = (kRoleWarps + 4) * 32;   // and a group of four for copies and products
-// Registers after the split: two groups of 128 threads take 208, the third 80, together 63 488 of the
+// Registers after the split: two groups of 128 threads take 200, the third 104, together 64 512 of the
 // 168 x 384 = 64 512 that the block is launched with.
-constexpr int kRegsRow = 208, kRegsRest = 80;
-constexpr int kFirstK = 6;              // of the eight 16-key steps of P V, those that start early
-constexpr int kMassPolyOf = 3;          // of every 8 pairs of the weights' kernel
-constexpr int kPolyOf = 4;              // of every 16 exponential pairs, those taken by polynomial
+constexpr int kRegsRow = 200, kRegsRest = 104;
+// The weights' kernel has no registers to spare for and four groups of row warps: two tiles, two TMEM
+// buffers each (four warps a scheduler instead of two took 32 768 positions of 32/8 heads from 6.0 to 4.9 ms)
+constexpr int kMassWarps = 16;
+constexpr int kMassThreads = (kMassWarps + 4) * 32;
+constexpr int kMassPolyOf = 1;          // of every 8 pairs of the weights' kernel
 
 struct PromptArgs {
   const int32_t* cu;      // [B + 1]
@@ -47,7 +51,7 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-// 2^x of two arguments without the special-function unit, whose rate bounds both kernels: x = n + f with
+// 2^x of two arguments without the special-function unit: x = n + f with
 // n the nearest integer, taken by adding 1.5 x 2^23, and a polynomial of degree 5 in f in [-1/2, 1/2]
 // (least maximal relative error, fitted by iteratively reweighted least squares: 7.5e-8, 2.1e-7 evaluated in
 // float32; ex2.approx has 2e-7); n is added to the exponent. Arguments from -127 up to 8.
@@ -80,13 +84,31 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// A operand in TMEM (16-bit pairs, one row a lane), B in shared memory
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+// The issuing warp runs its loops with all lanes and only the instructions themselves are one lane's:
+// so loop counters and descriptors stay warp-uniform, which the instructions want them to be (in a
+// one-lane branch every operand is moved over first: 2.05 instead of 1.94 ms at 16 384 positions).
+__device__ __forceinline__ void mma_f16_by(bool leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((uint32_t)leader)
+      : "memory");
+}
+// A operand in TMEM (16-bit pairs, one row a lane), B in shared memory
+__device__ __forceinline__ void mma_f16_ts_by(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((uint32_t)leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_by(bool leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"((uint32_t)leader)
       : "memory");
 }
 
@@ -155,8 +177,11 @@ struct TileRef {
 // call does nothing.
 __device__ TileRef find_tile(const PromptArgs& a, int P, int rank, bool from_end) {
   const int lane = threadIdx.x & 31;
-  int most = 0, bad = 0x7fffffff;
-  for (int b = lane; b < a.B; b += 32) {
+  // the bounds of the lane's first sequence stay in registers: most batches have no more than 32
+  const int s0 = lane < a.B ? a.cu[lane] : 0, e0 = lane < a.B ? a.cu[lane + 1] : 0;
+  const int tiles0 = (e0 - s0 + P - 1) / P;
+  int most = tiles0, bad = s0 < 0 || e0 < s0 || e0 > a.T ? lane : 0x7fffffff;
+  for (int b = lane + 32; b < a.B; b += 32) {
     const int s = a.cu[b], e = a.cu[b + 1];
     if (s < 0 || e < s || e > a.T) bad = min(bad, b);
     most = max(most, (e - s + P - 1) / P);
@@ -169,8 +194,8 @@ __device__ TileRef find_tile(const PromptArgs& a, int P, int rank, bool from_end
     return t;
   }
   auto at_least = [&](int w) {
-    int f = 0;
-    for (int b = lane; b < a.B; b += 32) f += max(0, (a.cu[b + 1] - a.cu[b] + P - 1) / P - w + 1);
+    int f = max(0, tiles0 - w + 1);
+    for (int b = lane + 32; b < a.B; b += 32) f += max(0, (a.cu[b + 1] - a.cu[b] + P - 1) / P - w + 1);
     return __reduce_add_sync(0xffffffffu, f);
   };
   if (most == 0 || at_least(1) <= rank) return t;
@@ -182,12 +207,13 @@ __device__ TileRef find_tile(const PromptArgs& a, int P, int rank, bool from_end
   int r = rank - (lo < most ? at_least(lo + 1) : 0);
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    const int n = b < a.B ? a.cu[b + 1] - a.cu[b] : 0, tiles = (n + P - 1) / P;
+    const int s = b0 == 0 ? s0 : b < a.B ? a.cu[b] : 0, n = (b0 == 0 ? e0 : b < a.B ? a.cu[b + 1] : 0) - s;
+    const int tiles = (n + P - 1) / P;
     const uint32_t has = __ballot_sync(0xffffffffu, tiles >= lo);
     if (r < __popc(has)) {
       const bool mine = (has >> lane & 1) && __popc(has & ((1u << lane) - 1u)) == r;
       const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-      t.start = __shfl_sync(0xffffffffu, b < a.B ? a.cu[b] : 0, src);
+      t.start = __shfl_sync(0xffffffffu, s, src);
       t.len = __shfl_sync(0xffffffffu, n, src);
       t.tile = from_end ? __shfl_sync(0xffffffffu, tiles, src) - lo : lo - 1;
       return t;
@@ -201,8 +227,8 @@ __device__ TileRef find_tile(const PromptArgs& a, int P, int rank, bool from_end
 // prompt attention
 // ---------------------------------------------------------------------------------------
 
-// A CTA owns two tiles of one kv head, 2 PT consecutive positions, and streams the keys and values
-// they see through a ring of 128-row tiles. Warp roles:
+// A persistent CTA walks items, each two tiles of one kv head, 2 PT consecutive positions, and streams
+// the keys and values they see through a ring of 128-row tiles. Warp roles:
 //   warps 0-3, 4-7  softmax of tile 0, tile 1: a thread owns a row (a TMEM lane). It reads the
 //                   row's 128 scores, keeps the running maximum m and sum l of exp2(c s - c m),
 //                   and writes the weights as 16-bit pairs over the scores. m only follows the true
@@ -210,6 +236,14 @@ __device__ TileRef find_tile(const PromptArgs& a, int P, int rank, bool from_end
 //   warp 8          TMA: both query tiles, then K_0 V_0 K_1 V_1 ...
 //   warp 9          tcgen05.mma: S_t = Q_t K^T, O_t += P_t V, the tiles in turn, so one tile's
 //                   softmax runs under the other's products.
+//   warp 10         finds the items, dealt out in falling work, there and back (c, 2G - 1 - c, 2G + c ...
+//                   for CTA c of G), so every CTA gets about the same.
+// The roles pass items on through a ring, so the next item's loads and first products run while the
+// softmax warps still write the last one out (four prompts of 2048, 32/8 heads: 197 us with a CTA an
+// item, 157 us this way).
+// What bounds it: not the tensor pipe (32 products of 64 cycles a round of two tiles, of some 3400) but a
+// tile's way round: 1800 cycles of softmax, 1024 of exponentials among them, then P V and the next
+// scores, whose issue waits for the pipe, with a wait and a commit between them.
 // TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each; P_t lies over the first half of S_t (the products
 // that read it are issued before those that write the next scores).
 template <int D>
@@ -217,7 +251,13 @@ struct AttendSmem {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kBoxBytes;
   static constexpr int NS = D == 128 ? 5 : 6;     // ring stages
-  static constexpr int BYTES = 1024 + (2 + NS) * TILE + 256;
+  static constexpr int BYTES = 1024 + (2 + NS) * TILE + 512;
+};
+
+constexpr int kItems = 3;       // items in flight between the roles
+
+struct ItemRef {
+  int start, len, pos0, kvh;    // first row and tokens of the sequence, the item's first position; len 0: the end
 };
 
 template <int D, bool BF16>
@@ -232,35 +272,41 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * S::TILE;
   uint64_t* qfull = reinterpret_cast<uint64_t*>(sKV + S::NS * S::TILE);   // [2]
-  uint64_t* full = qfull + 2;                                             // [NS]
+  uint64_t* qempty = qfull + 2;                                           // [2]
+  uint64_t* full = qempty + 2;                                            // [NS]
   uint64_t* empty = full + S::NS;                                         // [NS]
   uint64_t* sfull = empty + S::NS;                                        // [2] scores in TMEM
-  uint64_t* pfull = sfull + 2;                                            // [2][2] weights in TMEM: 96, 128 columns
-  uint64_t* odone = pfull + 4;                                            // [2] P V added
-  uint64_t* vclean = odone + 2;                                           // foreign rows of the last V cleared
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vclean + 1);
+  uint64_t* pfull = sfull + 2;                                            // [2] weights in TMEM
+  uint64_t* odone = pfull + 2;                                            // [2] P V added
+  uint64_t* ofree = odone + 2;                                            // [2] output read
+  uint64_t* vclean = ofree + 2;                                           // foreign rows of the last V cleared
+  uint64_t* drain = vclean + 1;                                           // every product done
+  uint64_t* ifull = drain + 1;                                            // [kItems]
+  uint64_t* iempty = ifull + kItems;                                      // [kItems]
+  ItemRef* sItem = reinterpret_cast<ItemRef*>(iempty + kItems);           // [kItems]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sItem + kItems);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* sTile = reinterpret_cast<int*>(tmem_slot + 2);                     // [3]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x % a.Hkv;
-  if (warp == 0) {
-    const TileRef t = find_tile(a, 2 * a.PT, blockIdx.x / a.Hkv, false);
-    if (lane == 0) sTile[0] = t.start, sTile[1] = t.len, sTile[2] = t.tile;
-  }
-  if (threadIdx.x == 32) {
+  if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 1);
+      mbar_init(&qempty[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[2 * i], 4);
-      mbar_init(&pfull[2 * i + 1], 4);
+      mbar_init(&pfull[i], 4);
       mbar_init(&odone[i], 1);
+      mbar_init(&ofree[i], 4);
     }
     for (int s = 0; s < S::NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(vclean, 4);
+    mbar_init(drain, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&ifull[i], 1);
+      mbar_init(&iempty[i], kRoleWarps + 2);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -269,135 +315,193 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int start = sTile[0], len = sTile[1], pos0 = sTile[2] * 2 * a.PT;
-  // key tiles that each query tile sees: up to its last position inside the sequence
-  int nt[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int end = min(len, pos0 + (t + 1) * a.PT);
-    nt[t] = pos0 + t * a.PT < len ? (end + kTileM - 1) / kTileM : 0;
-  }
-  const int N = max(nt[0], nt[1]);
-  // the last key tile holds rows behind the sequence: their weights are 0, but 0 x NaN is not
-  const bool dirty = N * kTileM > len;
-  const int clears = nt[1] == N ? 1 : 0;   // the group that sees the last tile clears those rows
+
+  auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
+    return wait_or_abort(bar, parity & 1, abort_flag, a.status, where);
+  };
+  // key tiles that query tile t of an item sees: up to its last position inside the sequence
+  auto key_tiles = [&](const ItemRef& it, int t) {
+    const int first = it.pos0 + t * a.PT;
+    return first < it.len ? (min(it.len, first + a.PT) + kTileM - 1) / kTileM : 0;
+  };
 
   if (warp >= kRoleWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (len > 0 && warp == 8) {
-      if (lane == 0) {
-        for (int t = 0; t < 2; ++t) {
-          if (nt[t] == 0) continue;
+    if (warp == 10) {
+      // ---- items ----
+      for (int j = 0;; ++j) {
+        const int G = gridDim.x, c = blockIdx.x, s = j % kItems;
+        const int item = j * G + (j & 1 ? G - 1 - c : c);
+        const TileRef t = find_tile(a, 2 * a.PT, item / a.Hkv, false);
+        if (!__all_sync(0xffffffffu, wait(&iempty[s], (j / kItems) ^ 1, 5011))) break;
+        if (lane == 0) {
+          sItem[s] = ItemRef{t.start, t.len, t.tile * 2 * a.PT, item % a.Hkv};
+          mbar_arrive(&ifull[s]);
+        }
+        if (t.len == 0) break;
+      }
+    } else if (warp == 8 && lane == 0) {
+      // ---- copies ----
+      int ring = 0, used[2] = {0, 0};    // tiles through the ring, items that had query tile t
+      for (int j = 0;; ++j) {
+        const int slot = j % kItems;
+        if (!wait(&ifull[slot], j / kItems, 5012)) break;
+        const ItemRef it = sItem[slot];
+        mbar_arrive(&iempty[slot]);
+        if (it.len == 0) break;
+        const int N = max(key_tiles(it, 0), key_tiles(it, 1));
+        bool ok = true;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (key_tiles(it, t) == 0) continue;
+          ok = wait(&qempty[t], used[t] ^ 1, 5013);
+          if (!ok) break;
+          ++used[t];
           mbar_arrive_expect_tx(&qfull[t], S::KB * a.G * a.PT * 128);
           for (int kb = 0; kb < S::KB; ++kb)
-            tma_load_3d(sQ + t * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + pos0 + t * a.PT, &qfull[t]);
+            tma_load_3d(sQ + t * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, it.kvh * a.G, it.start + it.pos0 + t * a.PT,
+                        &qfull[t]);
         }
-        for (int i = 0; i < 2 * N; ++i) {
-          const int s = i % S::NS;
-          if (!wait_or_abort(&empty[s], ((i / S::NS) & 1) ^ 1, abort_flag, a.status, 5001)) break;
+        for (int i = 0; i < 2 * N && ok; ++i, ++ring) {
+          const int s = ring % S::NS;
+          ok = wait(&empty[s], (ring / S::NS) ^ 1, 5001);
+          if (!ok) break;
           mbar_arrive_expect_tx(&full[s], S::TILE);
           const CUtensorMap* tm = (i & 1) ? &tmV : &tmK;
           for (int kb = 0; kb < S::KB; ++kb)
-            tma_load_3d(sKV + s * S::TILE + kb * kBoxBytes, tm, kb * 64, kvh, start + (i >> 1) * kTileM, &full[s]);
+            tma_load_3d(sKV + s * S::TILE + kb * kBoxBytes, tm, kb * 64, it.kvh, it.start + (i >> 1) * kTileM, &full[s]);
         }
+        if (!ok) break;
       }
-    } else if (len > 0 && warp == 9) {
-      if (lane == 0) {
-        auto wait_full = [&](int i) {
-          return wait_or_abort(&full[i % S::NS], (i / S::NS) & 1, abort_flag, a.status, 5002);
-        };
-        auto qk = [&](int t, int i) {       // S_t = Q_t K_i^T
-          const uint8_t* sK = sKV + ((2 * i) % S::NS) * S::TILE;
-  #pragma unroll
+    } else if (warp == 9) {
+      // ---- products ----
+      const bool lead = lane == 0;
+      // descriptors: the high words are constants, the low ones an address / 16 with the leading offset
+      const uint64_t dk0 = sdesc(smem_u32(sKV), 16, 1024), dv0 = sdesc(smem_u32(sKV), kBoxBytes, 1024);
+      const uint32_t hi_k = (uint32_t)(dk0 >> 32), hi_v = (uint32_t)(dv0 >> 32);
+      const uint32_t q_lo = (uint32_t)sdesc(smem_u32(sQ), 16, 1024);
+      auto desc = [](uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; };
+      auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
+        return __all_sync(0xffffffffu, wait_or_abort(bar, parity & 1, abort_flag, a.status, where));
+      };
+      int st = 0, ph = 0;                // the ring's next stage and its phase
+      int dirty_items = 0, used0 = 0, used1 = 0, blocks0 = 0, blocks1 = 0;
+      bool ok = true;
+      for (int j = 0; ok; ++j) {
+        const int slot = j % kItems;
+        ok = wait(&ifull[slot], j / kItems, 5014);
+        if (!ok) break;
+        const ItemRef it = sItem[slot];
+        __syncwarp();
+        if (lead) mbar_arrive(&iempty[slot]);
+        if (__shfl_sync(0xffffffffu, it.len, 0) == 0) break;
+        const int n0 = __shfl_sync(0xffffffffu, key_tiles(it, 0), 0), n1 = __shfl_sync(0xffffffffu, key_tiles(it, 1), 0);
+        const int N = max(n0, n1);
+        const bool dirty = N * kTileM > __shfl_sync(0xffffffffu, it.len, 0);
+        auto qk = [&](int t, bool last) {    // S_t = Q_t K^T, K in stage st
+          const uint32_t dk = (uint32_t)dk0 + st * (S::TILE >> 4);
+#pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * kBoxBytes + (k % 4) * 32;
-            mma_f16(tmem + t * kTileM, sdesc(smem_u32(sQ + t * S::TILE + off), 16, 1024),
-                    sdesc(smem_u32(sK + off), 16, 1024), ID_QK, k > 0 ? 1u : 0u);
+            const uint32_t off = ((k / 4) * kBoxBytes + (k % 4) * 32) >> 4;
+            mma_f16_by(lead, tmem + t * kTileM, desc(q_lo + t * (S::TILE >> 4) + off, hi_k), desc(dk + off, hi_k),
+                       ID_QK, k > 0 ? 1u : 0u);
           }
-          mma_commit(&sfull[t]);
+          // the next scores also tell the softmax warps that the products before them are done
+          mma_commit_by(lead, &sfull[t]);
+          if (last) mma_commit_by(lead, &qempty[t]);
         };
-        bool ok = wait_full(0);
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (nt[t] == 0) continue;
-          ok = wait_or_abort(&qfull[t], 0, abort_flag, a.status, 5003);
+        auto pv = [&](int t, int stage, int block, bool first) {   // O_t += P_t V
+          const uint32_t dv = (uint32_t)dv0 + stage * (S::TILE >> 4);
+          const uint32_t tO = tmem + 2 * kTileM + t * kTileM, tP = tmem + t * kTileM;
+          if (!wait(&pfull[t], block, 5005)) return false;
           tc_fence_after();
-          if (ok) qk(t, 0);
-        }
-        if (ok && S::NS < 2 * N) mma_commit(&empty[0]);
+#pragma unroll
+          for (int k = 0; k < kTileM / 16; ++k)
+            mma_f16_ts_by(lead, tO, tP + k * 8, desc(dv + k * 128, hi_v), ID_PV, !first || k > 0 ? 1u : 0u);
+          return true;
+        };
+        auto next = [&]() {
+          if (++st == S::NS) st = 0, ph ^= 1;
+        };
+        ok = wait(&full[st], ph, 5002);
+        if (ok && n0 > 0) ok = wait(&qfull[0], used0, 5003) && wait(&ofree[0], used0 ^ 1, 5015);
+        if (!ok) break;
+        tc_fence_after();
+        if (n0 > 0) qk(0, n0 == 1);
+        if (n1 > 0) ok = wait(&qfull[1], used1, 5003) && wait(&ofree[1], used1 ^ 1, 5015);
+        if (!ok) break;
+        tc_fence_after();
+        if (n1 > 0) qk(1, n1 == 1);
+        mma_commit_by(lead, &empty[st]);
+        next();
         for (int i = 0; i < N && ok; ++i) {
-          const int sv = (2 * i + 1) % S::NS;
-          ok = wait_full(2 * i + 1);
-          if (ok && i == N - 1 && dirty) ok = wait_or_abort(vclean, 0, abort_flag, a.status, 5004);
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (i < nt[t]) {
-              ok = wait_or_abort(&pfull[2 * t], i & 1, abort_flag, a.status, 5005);
-              if (!ok) break;
-              tc_fence_after();
-  #pragma unroll
-              for (int k = 0; k < kTileM / 16; ++k) {
-                if (k == kFirstK) {
-                  ok = wait_or_abort(&pfull[2 * t + 1], i & 1, abort_flag, a.status, 5010);
-                  if (!ok) break;
-                  tc_fence_after();
-                }
-                mma_f16_ts(tmem + 2 * kTileM + t * kTileM, tmem + t * kTileM + k * 8,
-                           sdesc(smem_u32(sKV + sv * S::TILE + k * 16 * 128), kBoxBytes, 1024), ID_PV,
-                           i > 0 || k > 0 ? 1u : 0u);
-              }
-              if (!ok) break;
-              mma_commit(&odone[t]);
-            }
-            if (t == 1 && 2 * i + 1 + S::NS < 2 * N) mma_commit(&empty[sv]);
-            if (i + 1 < N) {
-              if (t == 0) ok = wait_full(2 * i + 2);
-              if (ok && i + 1 < nt[t]) qk(t, i + 1);
-              if (t == 1 && 2 * i + 2 + S::NS < 2 * N) mma_commit(&empty[(2 * i + 2) % S::NS]);
-            }
+          // what the whole round needs is waited for first, while the softmax warps are at work
+          const int sv = st;
+          ok = wait(&full[sv], ph, 5002);
+          next();
+          if (ok && i + 1 < N) ok = wait(&full[st], ph, 5018);
+          if (ok && i == N - 1 && dirty) ok = wait(vclean, dirty_items, 5004);
+          if (ok && i < n0) ok = pv(0, sv, blocks0 + i, i == 0);
+          if (!ok) break;
+          if (i + 1 < n0) qk(0, i + 2 == n0);
+          else if (i + 1 == n0) mma_commit_by(lead, &odone[0]);
+          if (i < n1) ok = pv(1, sv, blocks1 + i, i == 0);
+          if (!ok) break;
+          if (i + 1 < n1) qk(1, i + 2 == n1);
+          else if (i + 1 == n1) mma_commit_by(lead, &odone[1]);
+          mma_commit_by(lead, &empty[sv]);
+          if (i + 1 < N) {
+            mma_commit_by(lead, &empty[st]);
+            next();
           }
         }
+        blocks0 += n0, blocks1 += n1;
+        used0 += n0 > 0, used1 += n1 > 0;
+        dirty_items += dirty;
       }
+      // the arrivals that the commits above announce land before the CTA leaves
+      mma_commit_by(lead, drain);
+      wait(drain, 0, 5016);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRow));
-    if (len > 0) {
-      // ---- softmax ----
-      const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
-      const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
-      const uint32_t tS = lane_addr + t * kTileM, tO = lane_addr + 2 * kTileM + t * kTileM;
-      const int pos = pos0 + t * a.PT + r / a.G;
-      const int n = nt[t];
+    // ---- softmax ----
+    const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t tS = lane_addr + t * kTileM, tO = lane_addr + 2 * kTileM + t * kTileM;
+    int ring = 0, blocks = 0, used = 0;  // tiles through the ring, blocks and items of this group, before the item
+    bool ok = true;
+    auto all = [&](uint64_t* bar, uint32_t parity, int where) { return __all_sync(0xffffffffu, wait(bar, parity, where)); };
+    for (int j = 0; ok; ++j) {
+      const int slot = j % kItems;
+      ok = all(&ifull[slot], j / kItems, 5017);
+      if (!ok) break;
+      const ItemRef it = sItem[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[slot]);
+      if (it.len == 0) break;
+      const int pos = it.pos0 + t * a.PT + r / a.G;
+      const int n = key_tiles(it, t), other = key_tiles(it, t ^ 1), N = max(n, other);
+      // The last key tile may hold rows behind the sequence: their weights are 0, but 0 x NaN is not.
+      // A group that sees that tile (the second one, if both do) clears them.
+      const bool clears = N * kTileM > it.len && n == N && (t == 1 || other < N);
       float m = -INFINITY, l = 0.f;
-      bool ok = true;
-      auto clear_foreign = [&]() {        // rows >= len of the last V tile
-        const int i = 2 * (N - 1) + 1;
-        if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&full[i % S::NS], (i / S::NS) & 1, abort_flag, a.status, 5006));
-        if (!ok) return;
-        uint8_t* sV = sKV + (i % S::NS) * S::TILE;
-        const int row0 = len - (N - 1) * kTileM;
-        for (int x = row0 * 8 + r; x < kTileM * 8; x += kTileM)
-          for (int kb = 0; kb < S::KB; ++kb)
-            *reinterpret_cast<uint4*>(sV + kb * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vclean);
-      };
-      for (int i = 0; i < n && ok; ++i) {
-        ok = __all_sync(0xffffffffu, wait_or_abort(&sfull[t], i & 1, abort_flag, a.status, 5007));
+      for (int i = 0; i < n; ++i) {
+        ok = all(&sfull[t], blocks + i, 5007);
         if (!ok) break;
         tc_fence_after();
         uint32_t v[kTileM];
-        const bool open = i * kTileM + kTileM - 1 <= pos0 + t * a.PT;   // every row sees every key
+        const bool open = i * kTileM + kTileM - 1 <= it.pos0 + t * a.PT;   // every row sees every key
         const int lim = pos - i * kTileM;   // columns 0..lim are seen
         float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
         auto rows_max = [&](int j0) {       // of 64 columns, four chains
           if (!open) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (j0 + j > lim) v[j0 + j] = 0xff800000u;
+            for (int x = 0; x < 64; ++x)
+              if (j0 + x > lim) v[j0 + x] = 0xff800000u;
           }
 #pragma unroll
-          for (int j = 0; j < 64; j += 2)
-            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(v[j0 + j]), __uint_as_float(v[j0 + j + 1]));
+          for (int x = 0; x < 64; x += 2)
+            mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(v[j0 + x]), __uint_as_float(v[j0 + x + 1]));
         };
         tmem_ld_x32(tS, v);
         tmem_ld_x32(tS + 32, v + 32);
@@ -414,78 +518,83 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (i > 0 && __any_sync(0xffffffffu, up)) {
           const float f = up ? ex2f((mo - m) * a.c) : 1.f;
           l *= f;
-          ok = __all_sync(0xffffffffu, wait_or_abort(&odone[t], (i - 1) & 1, abort_flag, a.status, 5008));
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll 1
-          for (int j = 0; j < D / 16; ++j) {
-            float o[16];
-            tmem_ld_x16(tO + 16 * j, reinterpret_cast<uint32_t*>(o));
+          for (int x = 0; x < D / 16; ++x) {
+            uint32_t o[16];
+            tmem_ld_x16(tO + 16 * x, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] *= f;
-            tmem_st_x16(tO + 16 * j, reinterpret_cast<const uint32_t*>(o));
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            tmem_st_x16(tO + 16 * x, o);
           }
         }
+        // The weights are rounded once, to the type of V, for the product; their sum is not.
         const float2 c2 = make_float2(a.c, a.c), mc2 = make_float2(-m * a.c, -m * a.c);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // The weights are rounded once, to the type of V, for the product; their sum is not. kPolyOf of
-        // every 16 pairs go to the FMA pipes (not in masked tiles: 0 there comes out as 2^-127).
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
 #pragma unroll
-          for (int j = 32 * q4; j < 32 * q4 + 32; j += 2) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, mc2);
-            float2 e;
-            if ((j / 2) % 16 >= 16 - kPolyOf && open) e = ex2_poly(x);
-            else e = make_float2(ex2f(x.x), ex2f(x.y));
-            sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], e);
+          for (int x = 32 * q4; x < 32 * q4 + 32; x += 2) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c2, mc2);
+            const float2 e = make_float2(ex2f(y.x), ex2f(y.y));
+            sum[(x >> 1) & 1] = __fadd2_rn(sum[(x >> 1) & 1], e);
             if (BF16)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[j / 2]) : "f"(e.y), "f"(e.x));
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[x / 2]) : "f"(e.y), "f"(e.x));
             else
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[j / 2]) : "f"(e.y), "f"(e.x));
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[x / 2]) : "f"(e.y), "f"(e.x));
           }
           tmem_st_x16(tS + 16 * q4, v + 16 * q4);
-          if (q4 == kFirstK / 2 - 1 || q4 == 3) {      // the product starts on three quarters of the weights
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[2 * t + (q4 == 3)]);
-          }
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[t]);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (i == N - 1 && dirty && t == clears) clear_foreign();
-      }
-      if (n > 0 && ok)
-        ok = __all_sync(0xffffffffu, wait_or_abort(&odone[t], (n - 1) & 1, abort_flag, a.status, 5009));
-      if (n > 0 && ok) {
-        tc_fence_after();
-        const float inv = 1.f / l;
-        const bool mine = r < a.G * a.PT && pos < len;
-        const size_t row = (size_t)(start + pos) * a.Hq + kvh * a.G + r % a.G;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * 2);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          uint32_t o[32];
-          tmem_ld_x32(tO + 32 * j, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const float lo = __uint_as_float(o[x]) * inv, hi = __uint_as_float(o[x + 1]) * inv;
-            if (BF16)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
-            else
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
-          }
-          if (mine) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              dst[j * 4 + x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-          }
+        if (clears && i == N - 1) {
+          const int last = ring + 2 * N - 1;
+          ok = all(&full[last % S::NS], last / S::NS, 5006);
+          if (!ok) break;
+          uint8_t* sV = sKV + (last % S::NS) * S::TILE;
+          for (int x = (it.len - (N - 1) * kTileM) * 8 + r; x < kTileM * 8; x += kTileM)
+            for (int kb = 0; kb < S::KB; ++kb)
+              *reinterpret_cast<uint4*>(sV + kb * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(vclean);
         }
-        if (mine && a.lse) a.lse[row] = (m * a.c + log2f(l)) * 0.693147180559945309f;
       }
-  
+      if (!ok) break;
+      ring += 2 * N;
+      blocks += n;
+      if (n == 0) continue;
+      // ---- the item's rows ----
+      ok = all(&odone[t], used++, 5009);
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = 1.f / l;
+      const bool mine = r < a.G * a.PT && pos < it.len;
+      const size_t row = (size_t)(it.start + pos) * a.Hq + it.kvh * a.G + r % a.G;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * 2);
+      uint32_t o[D];
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) tmem_ld_x32(tO + 32 * x, o + 32 * x);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ofree[t]);           // the next item's products may begin
+#pragma unroll
+      for (int x = 0; x < D; x += 2) {
+        const float lo = __uint_as_float(o[x]) * inv, hi = __uint_as_float(o[x + 1]) * inv;
+        if (BF16)
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
+        else
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
+      }
+      if (mine) {
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        if (a.lse) a.lse[row] = (m * a.c + log2f(l)) * 0.693147180559945309f;
+      }
     }
   }
   tc_fence_before();
@@ -512,12 +621,12 @@ struct MassSmem {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kBoxBytes;
   static constexpr int NS = 3;
-  static constexpr int NB = 4;                       // lse rows in flight (a power of two)
-  static constexpr int BYTES = 1024 + (2 + NS) * TILE + (NB + 2) * kTileM * 4 + 256;
+  static constexpr int NB = 8;                       // lse rows in flight: two a group
+  static constexpr int BYTES = 1024 + (2 + NS) * TILE + (NB + 4) * kTileM * 4 + 256;
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kPromptThreads, 1)
+__global__ void __launch_bounds__(kMassThreads, 1)
     prompt_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, PromptArgs a,
                        int ranks) {
   using S = MassSmem<D>;
@@ -526,9 +635,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sK = smem;
   uint8_t* sQ = smem + 2 * S::TILE;
-  float* sL = reinterpret_cast<float*>(sQ + S::NS * S::TILE);             // [2][2][128]: per group, double
-  float* sSum = sL + S::NB * kTileM;                                      // [256] for the cluster's first CTA
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(sSum + 2 * kTileM);
+  float* sL = reinterpret_cast<float*>(sQ + S::NS * S::TILE);             // [4][2][128]: per group, double
+  float* sSum = sL + S::NB * kTileM;                                      // [4][128]: the groups' sums
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(sSum + 4 * kTileM);
   uint64_t* full = kfull + 1;                                             // [NS]
   uint64_t* empty = full + S::NS;                                         // [NS]
   uint64_t* sfull = empty + S::NS;                                        // [2 tiles][2]
@@ -556,7 +665,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(tmem_slot, kTmemAll);
+  if (warp == kMassWarps + 1) tmem_alloc(tmem_slot, kTmemAll);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -567,7 +676,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int qt0 = key0 / a.PT + rank, qt1 = (len + a.PT - 1) / a.PT;
   const int N = len > 0 && qt1 > qt0 ? (qt1 - qt0 + ranks - 1) / ranks : 0;
 
-  if (N > 0 && warp == 8) {
+  if (N > 0 && warp == kMassWarps) {
     if (lane == 0) {
       mbar_arrive_expect_tx(kfull, two * S::TILE);
       for (int t = 0; t < two; ++t)
@@ -581,7 +690,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           tma_load_3d(sQ + s * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + (qt0 + i * ranks) * a.PT, &full[s]);
       }
     }
-  } else if (N > 0 && warp == 9) {
+  } else if (N > 0 && warp == kMassWarps + 1) {
     if (lane == 0 && wait_or_abort(kfull, 0, abort_flag, a.status, 5102)) {
       bool ok = true;
       for (int i = 0; i < N && ok; ++i) {
@@ -602,13 +711,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (i + S::NS < N) mma_commit(&empty[s]);
       }
     }
-  } else if (N > 0 && warp < kRoleWarps) {
-    const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
+  } else if (N > 0 && warp < kMassWarps) {
+    const int grp = warp >> 2, t = grp >> 1, b = grp & 1, q = warp & 3, r = q * 32 + lane;
     const int key = key0 + t * kTileM + r;
     const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
     const int gr = threadIdx.x & 127;                    // the query row whose lse this thread fetches
     const int gp = gr / a.G, gh = gr % a.G;
-    float* gL = sL + t * 2 * kTileM;                     // -log2(e) lse, double-buffered
+    float* gL = sL + grp * 2 * kTileM;                   // -log2(e) lse, double-buffered
     const int rows = a.G * a.PT;
     auto fetch = [&](int i) -> float {
       const int p = (qt0 + i * ranks) * a.PT + gp;
@@ -616,17 +725,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                  ? a.lse_in[(size_t)(start + p) * a.Hq + kvh * a.G + gh] * -1.4426950408889634f
                  : 0.f;
     };
-    float next = t < two ? fetch(0) : 0.f;
+    float next = t < two && b < N ? fetch(b) : 0.f;
     // A key of a long prompt adds up a hundred thousand weights: each tile's 128 are summed apart and
     // join the total with their rounding carried along (one plain float32 sum was off by 2e-5 of the
     // whole at 16 000 positions, this one by the scores' own error).
     float total = 0.f, carry = 0.f;
     const float2 c2 = make_float2(a.c, a.c);
-    for (int i = 0; t < two && i < N; ++i) {
-      const int b = i & 1;
-      gL[b * kTileM + gr] = next;
-      if (i + 1 < N) next = fetch(i + 1);
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+    for (int i = b; t < two && i < N; i += 2) {        // every other query tile: those of this buffer
+      float* nl = gL + (i >> 1 & 1) * kTileM;
+      nl[gr] = next;
+      if (i + 2 < N) next = fetch(i + 2);
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
       if (!__all_sync(0xffffffffu, wait_or_abort(&sfull[2 * t + b], (i >> 1) & 1, abort_flag, a.status, 5105))) break;
       tc_fence_after();
       const int p0 = (qt0 + i * ranks) * a.PT;
@@ -640,7 +749,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j < 3) tmem_ld_x32(tS + 32 * (j + 1), v[(j + 1) & 1]);   // under way during these
-          const float4* bias = reinterpret_cast<const float4*>(gL + b * kTileM + 32 * j);
+          const float4* bias = reinterpret_cast<const float4*>(nl + 32 * j);
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             const float4 w = bias[x / 4];
@@ -663,7 +772,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
-            const float e = ex2f(fmaf(__uint_as_float(v[x]), a.c, gL[b * kTileM + j + x]));
+            const float e = ex2f(fmaf(__uint_as_float(v[x]), a.c, nl[j + x]));
             if (j + x >= c_lo && j + x < c_hi) acc[x & 1].x += e;
           }
         }
@@ -675,23 +784,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       carry = __fsub_rn(__fsub_rn(sum, total), y);
       total = sum;
     }
-    if (ranks > 1) sSum[t * kTileM + r] = total;
-    else if (t < two && key < len) a.mass[(size_t)(start + key) * a.Hkv + kvh] = total;
+    sSum[grp * kTileM + r] = total;
   }
-  if (ranks > 1) {
-    if (N == 0 && threadIdx.x < 2 * kTileM) sSum[threadIdx.x] = 0.f;
-    __syncwarp();
-    cluster_sync_all();
-    if (rank == 0 && len > 0 && threadIdx.x < 2 * kTileM && key0 + (int)threadIdx.x < len) {
-      float total = 0.f;
-      for (int r = 0; r < ranks; ++r) total += ld_cluster(sSum + threadIdx.x, r);
-      a.mass[(size_t)(start + key0 + threadIdx.x) * a.Hkv + kvh] = total;
-    }
-    cluster_sync_all();                  // no CTA leaves while its sums are read
+  __syncwarp();
+  if (ranks > 1) cluster_sync_all(); else __syncthreads();
+  if (rank == 0 && len > 0 && threadIdx.x < 2 * kTileM && key0 + (int)threadIdx.x < len) {
+    const float* sums = sSum + (threadIdx.x >> 7) * 2 * kTileM + (threadIdx.x & 127);
+    float total = 0.f;
+    for (int r = 0; r < ranks; ++r)      // ranks behind the last query tile have nothing to add
+      if (qt0 + r < qt1) total += ranks > 1 ? ld_cluster(sums, r) + ld_cluster(sums + kTileM, r) : sums[0] + sums[kTileM];
+    a.mass[(size_t)(start + key0 + threadIdx.x) * a.Hkv + kvh] = total;
   }
+  if (ranks > 1) cluster_sync_all();     // no CTA leaves while its sums are read
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMassWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemAll);
   }
@@ -722,7 +829,7 @@ int check_prompt(int B, int T, int Hq, int Hkv, int D, int dtype) {
   if (dtype != QE_FP16 && dtype != QE_BF16) return QE_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || Hq / Hkv > QE_MAX_G) return QE_ERR_UNSUPPORTED_SHAPE;
   // CTAs of a launch, positions of 2 floor(128 / G) each
-  if (((long long)T / 32 + B) * Hkv >= (1ll << 31) || T > (1 << 30)) return QE_ERR_UNSUPPORTED_SHAPE;
+  if (((long long)T / 32 + B) * Hkv >= (1ll << 30) || T > (1 << 30)) return QE_ERR_UNSUPPORTED_SHAPE;
   return QE_OK;
 }
 
@@ -737,8 +844,10 @@ int launch_attend(const void* q, const void* k, const void* v, long long qs, lon
   using S = AttendSmem<D>;
   auto kern = prompt_attend_kernel<D, BF16>;
   static QeOnce once;
+  static int sms_of[QE_MAX_DEVICES];
   int dev = 0;
-  int e = qe_once_per_device(once, &dev, [&](int) {
+  int e = qe_once_per_device(once, &dev, [&](int d) {
+    QE_CUDA_TRY(cudaDeviceGetAttribute(&sms_of[d], cudaDevAttrMultiProcessorCount, d));
     QE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES));
     return QE_OK;
   });
@@ -747,8 +856,8 @@ int launch_attend(const void* q, const void* k, const void* v, long long qs, lon
   if ((e = make_map3(&tmQ, q, BF16, D, a.Hq, a.T, qs, a.G, a.PT))) return e;
   if ((e = make_map3(&tmK, k, BF16, D, a.Hkv, a.T, ks, 1, kTileM))) return e;
   if ((e = make_map3(&tmV, v, BF16, D, a.Hkv, a.T, vs, 1, kTileM))) return e;
-  const int tiles = a.T / (2 * a.PT) + (a.B < a.T ? a.B : a.T);
-  kern<<<tiles * a.Hkv, kPromptThreads, S::BYTES, st>>>(tmQ, tmK, tmV, a);
+  const long long items = ((long long)a.T / (2 * a.PT) + (a.B < a.T ? a.B : a.T)) * a.Hkv;
+  kern<<<(int)(items < sms_of[dev] ? items : sms_of[dev]), kPromptThreads, S::BYTES, st>>>(tmQ, tmK, tmV, a);
   return cudaGetLastError() == cudaSuccess ? QE_OK : QE_ERR_CUDA;
 }
 
@@ -777,7 +886,7 @@ int launch_mass(const void* q, const void* k, long long qs, long long ks, Prompt
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3((unsigned)items * ranks);
-  cfg.blockDim = dim3(kPromptThreads);
+  cfg.blockDim = dim3(kMassThreads);
   cfg.dynamicSmemBytes = S::BYTES;
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeClusterDimension;
