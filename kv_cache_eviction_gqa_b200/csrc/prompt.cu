@@ -23,16 +23,13 @@ using namespace tc;
 constexpr int kTileM = 128;             // packed query rows, keys, and accumulator columns of a tile
 constexpr int kBoxBytes = 128 * 128;    // 128 rows x 64 16-bit elements
 constexpr int kTmemAll = 512;
-constexpr int kRoleWarps = 8;           // two groups of four: one TMEM lane a thread, a tile a group
-constexpr int kPromptThreads = (kRoleWarps + 4) * 32;   // and a group of four for copies and products
-// Registers after the split: two groups of 128 threads take 200, the third 104, together 64 512 of the
-// 168 x 384 = 64 512 that the block is launched with.
-constexpr int kRegsRow = 200, kRegsRest = 104;
-// The weights' kernel has no registers to spare for and four groups of row warps: two tiles, two TMEM
-// buffers each (four warps a scheduler instead of two took 32 768 positions of 32/8 heads from 6.0 to 4.9 ms)
-constexpr int kMassWarps = 16;
-constexpr int kMassThreads = (kMassWarps + 4) * 32;
-constexpr int kMassPolyOf = 1;          // of every 8 pairs of the weights' kernel
+// Both kernels have sixteen warps that hold scores, four a scheduler, beside four for copies, products
+// and bookkeeping: eight (attention: a whole row a thread; weights: both buffers a group) left more of
+// the special-function unit idle (16 384 positions, 32/8 heads, D 128: attention 1.86 instead of 1.77 ms;
+// weights at 32 768: 6.0 instead of 4.9 ms).
+constexpr int kRoleWarps = 16;
+constexpr int kPromptThreads = (kRoleWarps + 4) * 32;
+constexpr int kMassPolyOf = 1;          // of every 8 pairs of the weights' kernel, those taken by polynomial
 
 struct PromptArgs {
   const int32_t* cu;      // [B + 1]
@@ -142,13 +139,6 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* v) {
       : QE_R8(v, 0), QE_R8(v, 8)
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::QE_W8(v, 0),
-      QE_W8(v, 8), QE_W8(v, 16), QE_W8(v, 24), "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -229,29 +219,35 @@ __device__ TileRef find_tile(const PromptArgs& a, int P, int rank, bool from_end
 
 // A persistent CTA walks items, each two tiles of one kv head, 2 PT consecutive positions, and streams
 // the keys and values they see through a ring of 128-row tiles. Warp roles:
-//   warps 0-3, 4-7  softmax of tile 0, tile 1: a thread owns a row (a TMEM lane). It reads the
-//                   row's 128 scores, keeps the running maximum m and sum l of exp2(c s - c m),
-//                   and writes the weights as 16-bit pairs over the scores. m only follows the true
-//                   maximum when that has risen by 2^8; then the row of O is rescaled in TMEM.
-//   warp 8          TMA: both query tiles, then K_0 V_0 K_1 V_1 ...
-//   warp 9          tcgen05.mma: S_t = Q_t K^T, O_t += P_t V, the tiles in turn, so one tile's
+//   warps 0-15      softmax, eight a tile: a thread owns half a row (64 columns of a TMEM lane). It reads
+//                   its scores, agrees with the thread of the other half on the running maximum m,
+//                   sums exp2(c s - c m) and writes the weights as 16-bit pairs over the scores. m only
+//                   follows the true maximum when that has risen by 2^8; then the row of O is
+//                   rescaled in TMEM.
+//   warp 16         TMA: both query tiles, then K_0 V_0 K_1 V_1 ...
+//   warp 17         tcgen05.mma: S_t = Q_t K^T, O_t += P_t V, the tiles in turn, so one tile's
 //                   softmax runs under the other's products.
-//   warp 10         finds the items, dealt out in falling work, there and back (c, 2G - 1 - c, 2G + c ...
+//   warp 18         finds the items, dealt out in falling work, there and back (c, 2G - 1 - c, 2G + c ...
 //                   for CTA c of G), so every CTA gets about the same.
+//   warp 19         waits for what a tile's products need besides the weights (keys and values in place),
+//                   so that warp 17 has one wait a tile.
 // The roles pass items on through a ring, so the next item's loads and first products run while the
 // softmax warps still write the last one out (four prompts of 2048, 32/8 heads: 197 us with a CTA an
 // item, 157 us this way).
-// What bounds it: not the tensor pipe (32 products of 64 cycles a round of two tiles, of some 3400) but a
-// tile's way round: 1800 cycles of softmax, 1024 of exponentials among them, then P V and the next
-// scores, whose issue waits for the pipe, with a wait and a commit between them.
+// What bounds it: a tile's way round, some 3500 cycles, of which the tensor pipe has 1024 for either tile:
+// reading and searching the scores takes 400, the weights 1500 (1024 of them exponentials at the
+// special-function unit's rate; moving some to a polynomial gained nothing), P V and the next scores
+// 1150, hand-overs the rest. S and P share TMEM, which O_0, O_1, S_0, S_1 fill, so the next scores
+// cannot start before P V. Two warps issuing products, one a tile, let the tiles run in step and was
+// slower (2.2 ms).
 // TMEM: S_0 | S_1 | O_0 | O_1, 128 columns each; P_t lies over the first half of S_t (the products
 // that read it are issued before those that write the next scores).
 template <int D>
 struct AttendSmem {
   static constexpr int KB = D / 64;
   static constexpr int TILE = KB * kBoxBytes;
-  static constexpr int NS = D == 128 ? 5 : 6;     // ring stages
-  static constexpr int BYTES = 1024 + (2 + NS) * TILE + 512;
+  static constexpr int NS = D == 128 ? 4 : 6;     // ring stages
+  static constexpr int BYTES = 1024 + (2 + NS) * TILE + 8 * kTileM * 4 + 512;
 };
 
 constexpr int kItems = 3;       // items in flight between the roles
@@ -271,12 +267,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * S::TILE;
-  uint64_t* qfull = reinterpret_cast<uint64_t*>(sKV + S::NS * S::TILE);   // [2]
+  float* sRow = reinterpret_cast<float*>(sKV + S::NS * S::TILE);          // [2][tile][half][128]
+  uint64_t* qfull = reinterpret_cast<uint64_t*>(sRow + 8 * kTileM);       // [2]
   uint64_t* qempty = qfull + 2;                                           // [2]
   uint64_t* full = qempty + 2;                                            // [NS]
   uint64_t* empty = full + S::NS;                                         // [NS]
   uint64_t* sfull = empty + S::NS;                                        // [2] scores in TMEM
-  uint64_t* pfull = sfull + 2;                                            // [2] weights in TMEM
+  uint64_t* pfull = sfull + 2;                                            // [2] weights in TMEM, V and the next K in place
   uint64_t* odone = pfull + 2;                                            // [2] P V added
   uint64_t* ofree = odone + 2;                                            // [2] output read
   uint64_t* vclean = ofree + 2;                                           // foreign rows of the last V cleared
@@ -293,24 +290,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&qfull[i], 1);
       mbar_init(&qempty[i], 1);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[i], 9);
       mbar_init(&odone[i], 1);
-      mbar_init(&ofree[i], 4);
+      mbar_init(&ofree[i], 8);
     }
     for (int s = 0; s < S::NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(vclean, 4);
+    mbar_init(vclean, 8);
     mbar_init(drain, 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&ifull[i], 1);
-      mbar_init(&iempty[i], kRoleWarps + 2);
+      mbar_init(&iempty[i], kRoleWarps + 3);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(tmem_slot, kTmemAll);
+  if (warp == kRoleWarps + 1) tmem_alloc(tmem_slot, kTmemAll);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -326,8 +323,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   };
 
   if (warp >= kRoleWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == 10) {
+    if (warp == kRoleWarps + 2) {
       // ---- items ----
       for (int j = 0;; ++j) {
         const int G = gridDim.x, c = blockIdx.x, s = j % kItems;
@@ -340,7 +336,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (t.len == 0) break;
       }
-    } else if (warp == 8 && lane == 0) {
+    } else if (warp == kRoleWarps + 3 && lane == 0) {
+      // ---- what a tile's products need besides its weights: V_i, K_{i + 1}, and no foreign rows ----
+      int ring = 0, dirty_items = 0, blocks0 = 0, blocks1 = 0;
+      bool ok = true;
+      for (int j = 0; ok; ++j) {
+        const int slot = j % kItems;
+        ok = wait(&ifull[slot], j / kItems, 5019);
+        if (!ok) break;
+        const ItemRef it = sItem[slot];
+        mbar_arrive(&iempty[slot]);
+        if (it.len == 0) break;
+        const int n0 = key_tiles(it, 0), n1 = key_tiles(it, 1), N = max(n0, n1);
+        const bool dirty = N * kTileM > it.len;
+        for (int i = 0; i < N && ok; ++i) {
+          const int v = ring + 2 * i + 1, k = v + 1;
+          ok = wait(&full[v % S::NS], v / S::NS, 5002);
+          if (ok && i + 1 < N) ok = wait(&full[k % S::NS], k / S::NS, 5018);
+          if (ok && i == N - 1 && dirty) ok = wait(vclean, dirty_items, 5004);
+          if (!ok) break;
+          if (i < n0) mbar_arrive(&pfull[0]);
+          if (i < n1) mbar_arrive(&pfull[1]);
+          // one arrival a phase: the next one when these products could start
+          if (i < n0) ok = wait(&pfull[0], blocks0 + i, 5020);
+          if (ok && i < n1) ok = wait(&pfull[1], blocks1 + i, 5020);
+        }
+        ring += 2 * N;
+        blocks0 += n0, blocks1 += n1;
+        dirty_items += dirty;
+      }
+    } else if (warp == kRoleWarps && lane == 0) {
       // ---- copies ----
       int ring = 0, used[2] = {0, 0};    // tiles through the ring, items that had query tile t
       for (int j = 0;; ++j) {
@@ -372,7 +397,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (!ok) break;
       }
-    } else if (warp == 9) {
+    } else if (warp == kRoleWarps + 1) {
       // ---- products ----
       const bool lead = lane == 0;
       // descriptors: the high words are constants, the low ones an address / 16 with the leading offset
@@ -384,7 +409,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         return __all_sync(0xffffffffu, wait_or_abort(bar, parity & 1, abort_flag, a.status, where));
       };
       int st = 0, ph = 0;                // the ring's next stage and its phase
-      int dirty_items = 0, used0 = 0, used1 = 0, blocks0 = 0, blocks1 = 0;
+      int used0 = 0, used1 = 0, blocks0 = 0, blocks1 = 0;
       bool ok = true;
       for (int j = 0; ok; ++j) {
         const int slot = j % kItems;
@@ -396,7 +421,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (__shfl_sync(0xffffffffu, it.len, 0) == 0) break;
         const int n0 = __shfl_sync(0xffffffffu, key_tiles(it, 0), 0), n1 = __shfl_sync(0xffffffffu, key_tiles(it, 1), 0);
         const int N = max(n0, n1);
-        const bool dirty = N * kTileM > __shfl_sync(0xffffffffu, it.len, 0);
         auto qk = [&](int t, bool last) {    // S_t = Q_t K^T, K in stage st
           const uint32_t dk = (uint32_t)dk0 + st * (S::TILE >> 4);
 #pragma unroll
@@ -434,13 +458,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         mma_commit_by(lead, &empty[st]);
         next();
         for (int i = 0; i < N && ok; ++i) {
-          // what the whole round needs is waited for first, while the softmax warps are at work
           const int sv = st;
-          ok = wait(&full[sv], ph, 5002);
           next();
-          if (ok && i + 1 < N) ok = wait(&full[st], ph, 5018);
-          if (ok && i == N - 1 && dirty) ok = wait(vclean, dirty_items, 5004);
-          if (ok && i < n0) ok = pv(0, sv, blocks0 + i, i == 0);
+          if (i < n0) ok = pv(0, sv, blocks0 + i, i == 0);
           if (!ok) break;
           if (i + 1 < n0) qk(0, i + 2 == n0);
           else if (i + 1 == n0) mma_commit_by(lead, &odone[0]);
@@ -456,19 +476,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         blocks0 += n0, blocks1 += n1;
         used0 += n0 > 0, used1 += n1 > 0;
-        dirty_items += dirty;
       }
       // the arrivals that the commits above announce land before the CTA leaves
       mma_commit_by(lead, drain);
       wait(drain, 0, 5016);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRow));
     // ---- softmax ----
-    const int t = warp >> 2, q = warp & 3, r = q * 32 + lane;
+    const int t = warp >> 3, half = warp >> 2 & 1, q = warp & 3, r = q * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
-    const uint32_t tS = lane_addr + t * kTileM, tO = lane_addr + 2 * kTileM + t * kTileM;
+    const uint32_t tS = lane_addr + t * kTileM, tO = lane_addr + 2 * kTileM + t * kTileM + half * (D / 2);
+    float* own_x = sRow + (t * 2 + half) * kTileM + r;            // what the two halves of a row exchange
+    const float* other_x = sRow + (t * 2 + (half ^ 1)) * kTileM + r;
+    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + q) : "memory"); };
     int ring = 0, blocks = 0, used = 0;  // tiles through the ring, blocks and items of this group, before the item
+    int side = 0;                        // exchanges alternate between two buffers: one is read when the other is written
     bool ok = true;
     auto all = [&](uint64_t* bar, uint32_t parity, int where) { return __all_sync(0xffffffffu, wait(bar, parity, where)); };
     for (int j = 0; ok; ++j) {
@@ -482,36 +504,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int pos = it.pos0 + t * a.PT + r / a.G;
       const int n = key_tiles(it, t), other = key_tiles(it, t ^ 1), N = max(n, other);
       // The last key tile may hold rows behind the sequence: their weights are 0, but 0 x NaN is not.
-      // A group that sees that tile (the second one, if both do) clears them.
+      // The warps of a tile that sees that one (the second, if both do) clear them.
       const bool clears = N * kTileM > it.len && n == N && (t == 1 || other < N);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
         ok = all(&sfull[t], blocks + i, 5007);
         if (!ok) break;
         tc_fence_after();
-        uint32_t v[kTileM];
+        uint32_t v[64];
         const bool open = i * kTileM + kTileM - 1 <= it.pos0 + t * a.PT;   // every row sees every key
-        const int lim = pos - i * kTileM;   // columns 0..lim are seen
+        const int lim = pos - i * kTileM - 64 * half;                      // columns 0..lim are seen
         float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
-        auto rows_max = [&](int j0) {       // of 64 columns, four chains
-          if (!open) {
-#pragma unroll
-            for (int x = 0; x < 64; ++x)
-              if (j0 + x > lim) v[j0 + x] = 0xff800000u;
-          }
-#pragma unroll
-          for (int x = 0; x < 64; x += 2)
-            mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(v[j0 + x]), __uint_as_float(v[j0 + x + 1]));
-        };
-        tmem_ld_x32(tS, v);
-        tmem_ld_x32(tS + 32, v + 32);
+        tmem_ld_x32(tS + 64 * half, v);
+        tmem_ld_x32(tS + 64 * half + 32, v + 32);
         tmem_wait_ld();
-        tmem_ld_x32(tS + 64, v + 64);       // under way while the first half is searched
-        tmem_ld_x32(tS + 96, v + 96);
-        rows_max(0);
-        tmem_wait_ld();
-        rows_max(64);
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        if (!open) {
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            if (x > lim) v[x] = 0xff800000u;
+        }
+#pragma unroll
+        for (int x = 0; x < 64; x += 2)
+          mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+        const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        // both halves' scores are in registers behind this point: the weights may lie over them
+        own_x[side] = mine;
+        meet();
+        const float top = fmaxf(mine, other_x[side]);
+        side ^= 4 * kTileM;
         const bool up = (top - m) * a.c > 8.f;         // true on the first tile (m = -inf)
         const float mo = m;
         if (up) m = top;
@@ -519,7 +539,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const float f = up ? ex2f((mo - m) * a.c) : 1.f;
           l *= f;
 #pragma unroll 1
-          for (int x = 0; x < D / 16; ++x) {
+          for (int x = 0; x < D / 32; ++x) {
             uint32_t o[16];
             tmem_ld_x16(tO + 16 * x, o);
             tmem_wait_ld();
@@ -532,18 +552,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const float2 c2 = make_float2(a.c, a.c), mc2 = make_float2(-m * a.c, -m * a.c);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-#pragma unroll
-          for (int x = 32 * q4; x < 32 * q4 + 32; x += 2) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c2, mc2);
-            const float2 e = make_float2(ex2f(y.x), ex2f(y.y));
-            sum[(x >> 1) & 1] = __fadd2_rn(sum[(x >> 1) & 1], e);
-            if (BF16)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[x / 2]) : "f"(e.y), "f"(e.x));
-            else
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[x / 2]) : "f"(e.y), "f"(e.x));
-          }
-          tmem_st_x16(tS + 16 * q4, v + 16 * q4);
+        for (int x = 0; x < 64; x += 2) {
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c2, mc2);
+          const float2 e = make_float2(ex2f(y.x), ex2f(y.y));
+          sum[(x >> 1) & 1] = __fadd2_rn(sum[(x >> 1) & 1], e);
+          if (BF16)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[x / 2]) : "f"(e.y), "f"(e.x));
+          else
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[x / 2]) : "f"(e.y), "f"(e.x));
+          if (x % 32 == 30) tmem_st_x16(tS + 32 * half + x / 32 * 16, v + x / 32 * 16);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -555,7 +572,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           ok = all(&full[last % S::NS], last / S::NS, 5006);
           if (!ok) break;
           uint8_t* sV = sKV + (last % S::NS) * S::TILE;
-          for (int x = (it.len - (N - 1) * kTileM) * 8 + r; x < kTileM * 8; x += kTileM)
+          for (int x = (it.len - (N - 1) * kTileM) * 8 + half * kTileM + r; x < kTileM * 8; x += 2 * kTileM)
             for (int kb = 0; kb < S::KB; ++kb)
               *reinterpret_cast<uint4*>(sV + kb * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
@@ -567,23 +584,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       ring += 2 * N;
       blocks += n;
       if (n == 0) continue;
-      // ---- the item's rows ----
+      // ---- the item's rows: this half's columns ----
+      own_x[side] = l;
+      meet();
+      l += other_x[side];
+      side ^= 4 * kTileM;
       ok = all(&odone[t], used++, 5009);
       if (!ok) break;
       tc_fence_after();
       const float inv = 1.f / l;
       const bool mine = r < a.G * a.PT && pos < it.len;
       const size_t row = (size_t)(it.start + pos) * a.Hq + it.kvh * a.G + r % a.G;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * 2);
-      uint32_t o[D];
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * 2 + half * D);
+      uint32_t o[D / 2];
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) tmem_ld_x32(tO + 32 * x, o + 32 * x);
+      for (int x = 0; x < D / 64; ++x) tmem_ld_x32(tO + 32 * x, o + 32 * x);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ofree[t]);           // the next item's products may begin
 #pragma unroll
-      for (int x = 0; x < D; x += 2) {
+      for (int x = 0; x < D / 2; x += 2) {
         const float lo = __uint_as_float(o[x]) * inv, hi = __uint_as_float(o[x + 1]) * inv;
         if (BF16)
           asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
@@ -592,14 +613,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       if (mine) {
 #pragma unroll
-        for (int x = 0; x < D / 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-        if (a.lse) a.lse[row] = (m * a.c + log2f(l)) * 0.693147180559945309f;
+        for (int x = 0; x < D / 16; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        if (a.lse && half == 0) a.lse[row] = (m * a.c + log2f(l)) * 0.693147180559945309f;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kRoleWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemAll);
   }
@@ -626,7 +647,7 @@ struct MassSmem {
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kMassThreads, 1)
+__global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_mass_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, PromptArgs a,
                        int ranks) {
   using S = MassSmem<D>;
@@ -665,7 +686,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMassWarps + 1) tmem_alloc(tmem_slot, kTmemAll);
+  if (warp == kRoleWarps + 1) tmem_alloc(tmem_slot, kTmemAll);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -676,7 +697,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   const int qt0 = key0 / a.PT + rank, qt1 = (len + a.PT - 1) / a.PT;
   const int N = len > 0 && qt1 > qt0 ? (qt1 - qt0 + ranks - 1) / ranks : 0;
 
-  if (N > 0 && warp == kMassWarps) {
+  if (N > 0 && warp == kRoleWarps) {
     if (lane == 0) {
       mbar_arrive_expect_tx(kfull, two * S::TILE);
       for (int t = 0; t < two; ++t)
@@ -690,7 +711,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           tma_load_3d(sQ + s * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + (qt0 + i * ranks) * a.PT, &full[s]);
       }
     }
-  } else if (N > 0 && warp == kMassWarps + 1) {
+  } else if (N > 0 && warp == kRoleWarps + 1) {
     if (lane == 0 && wait_or_abort(kfull, 0, abort_flag, a.status, 5102)) {
       bool ok = true;
       for (int i = 0; i < N && ok; ++i) {
@@ -711,7 +732,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         if (i + S::NS < N) mma_commit(&empty[s]);
       }
     }
-  } else if (N > 0 && warp < kMassWarps) {
+  } else if (N > 0 && warp < kRoleWarps) {
     const int grp = warp >> 2, t = grp >> 1, b = grp & 1, q = warp & 3, r = q * 32 + lane;
     const int key = key0 + t * kTileM + r;
     const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
@@ -798,7 +819,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   if (ranks > 1) cluster_sync_all();     // no CTA leaves while its sums are read
   tc_fence_before();
   __syncthreads();
-  if (warp == kMassWarps + 1) {
+  if (warp == kRoleWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemAll);
   }
@@ -886,7 +907,7 @@ int launch_mass(const void* q, const void* k, long long qs, long long ks, Prompt
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3((unsigned)items * ranks);
-  cfg.blockDim = dim3(kMassThreads);
+  cfg.blockDim = dim3(kPromptThreads);
   cfg.dynamicSmemBytes = S::BYTES;
   cfg.stream = st;
   at[0].id = cudaLaunchAttributeClusterDimension;
