@@ -687,6 +687,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     fence_mbar_init();
   }
   if (warp == kRoleWarps + 1) tmem_alloc(tmem_slot, kTmemAll);
+  // rows that no query fills (128 - G PT of them): zero scores, which their -inf bias makes nothing of
+  for (int x = a.G * a.PT * 8 + threadIdx.x; x < kTileM * 8; x += kPromptThreads)
+    for (int b = 0; b < S::NS * S::KB; ++b) *reinterpret_cast<uint4*>(sQ + b * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -744,7 +748,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int p = (qt0 + i * ranks) * a.PT + gp;
       return gr < rows && p < len
                  ? a.lse_in[(size_t)(start + p) * a.Hq + kvh * a.G + gh] * -1.4426950408889634f
-                 : 0.f;
+                 : -INFINITY;
     };
     float next = t < two && b < N ? fetch(b) : 0.f;
     // A key of a long prompt adds up a hundred thousand weights: each tile's 128 are summed apart and
@@ -760,7 +764,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (!__all_sync(0xffffffffu, wait_or_abort(&sfull[2 * t + b], (i >> 1) & 1, abort_flag, a.status, 5105))) break;
       tc_fence_after();
       const int p0 = (qt0 + i * ranks) * a.PT;
-      const bool open = p0 >= key0 + (t + 1) * kTileM - 1 && p0 + a.PT <= len && rows == kTileM;
+      const bool open = p0 >= key0 + (t + 1) * kTileM - 1 && p0 + a.PT <= len;
       const uint32_t tS = lane_addr + (2 * t + b) * kTileM;
       float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       if (open) {
@@ -899,11 +903,11 @@ int launch_mass(const void* q, const void* k, long long qs, long long ks, Prompt
   if ((e = make_map3(&tmQ, q, BF16, D, a.Hq, a.T, qs, a.G, a.PT))) return e;
   if ((e = make_map3(&tmK, k, BF16, D, a.Hkv, a.T, ks, 1, kTileM))) return e;
   const int items = (a.T / (2 * kTileM) + (a.B < a.T ? a.B : a.T)) * a.Hkv;
-  // Two items an SM and more balance by themselves, longest first. Below that the longest alone would
-  // decide: 8192 positions, 2 kv heads of 8: 949 us with one CTA for a tile of keys, the products of a
-  // 148th of the work being 110
+  // One and a half items an SM and more balance by themselves, longest first (four prompts of 2048, 8 kv
+  // heads: 94 us with one CTA an item, 107 with two); below that the longest alone would decide (8192
+  // positions, 2 kv heads of 8: 949 us with one, 167 with four; a cluster of eight starts late: 206).
   int ranks = 1;
-  while (ranks < 8 && items * ranks < 2 * sms_of[dev]) ranks *= 2;
+  while (ranks < 4 && 2 * items * ranks < 3 * sms_of[dev]) ranks *= 2;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3((unsigned)items * ranks);
