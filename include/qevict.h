@@ -509,7 +509,8 @@ QE_API int qe_int4_attend(const qe_int4_cache* cache, const void* q, long long q
  *     dst holds at least `budget` entries a unit.
  * All qe_int4_* errors (returned, nothing launched): QE_ERR_INVALID_ARG (null or misaligned pointer, bad
  * sizes or strides, budget < 1 or above dst's capacity, recent < 0, shared buffers),
- * QE_ERR_UNSUPPORTED_SHAPE (D not in {64, 128}, B * Hkv * max_pages * 16 >= 2^31). T == 0 does nothing.
+ * QE_ERR_UNSUPPORTED_SHAPE (D not in {64, 128}, B * Hkv * max_pages * 16 or n_pages * 16 >= 2^31). T == 0
+ * does nothing.
  * Asynchronous on `stream`; allocates nothing. */
 QE_API int qe_int4_evict(const qe_int4_cache* src, const qe_int4_cache* dst, int budget, int recent,
                          qe_stream_t stream);

@@ -600,34 +600,55 @@ def sekv_views(state: torch.Tensor, B: int, Hq: int, Hkv: int, n: int, D: int) -
 # ---------------------------------------------------------------------------------
 
 
-def _tokens(t: torch.Tensor, name: str, heads: int, D: int, dtype, T=None) -> int:
-    """Check a [T][heads][D] CUDA view whose tokens may be strided; its token stride in elements."""
-    if not t.is_cuda or t.dim() != 3 or t.dtype != dtype:
-        raise ValueError(f"{name} must be a 3-D {dtype} CUDA tensor")
-    if t.shape[1] != heads or t.shape[2] != D or (T is not None and t.shape[0] != T):
-        raise ValueError(f"{name} must have shape {(T, heads, D)}, got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+# These calls are also made for single tokens, where checking costs as much as computing: one pass
+# over each tensor's properties, messages only when something is wrong.
+
+
+def _tokens(t: torch.Tensor, name: str, T: int, heads: int, D: int, dtype, index: int) -> int:
+    """Check a [T][heads][D] view on device `index` whose tokens may be strided; its token stride."""
+    if t.dtype is not dtype or t.shape != (T, heads, D) or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(T, heads, D)} on cuda:{index}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != D and heads > 1):
         raise ValueError(f"the heads and elements of {name} must be contiguous within a token")
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    return s[0] if T > 1 else heads * D
 
 
-def _same_device(dev, *named):
-    for t, name in named:
-        if t is not None and t.get_device() != dev.index:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _plain(t: torch.Tensor, name: str, dtype, shape, index: int):
+    """Check a contiguous tensor on device `index`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 _HERE = contextlib.nullcontext()
 
 
-def _on(dev):
-    """The context in which calls go to dev (nothing to do when it is the current device)."""
-    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _on(index: int, stream=None):
+    """The context in which a call goes to a device and what it allocates belongs to its stream (nothing to
+    do for the current device's current stream)."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _raw(stream, dev) -> int:
-    """The CUDA stream of a torch stream, by default the current one of dev."""
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+def _raw(stream, index: int) -> int:
+    """The CUDA stream of a torch stream, by default the current one of the device."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _cuda_index(t: torch.Tensor, name: str) -> int:
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return i
+
+
+def _three(t: torch.Tensor, name: str):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, got {tuple(t.shape)}")
+    return t.shape
 
 
 def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, out=None, lse=None,
@@ -639,24 +660,28 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     float32, status [2] int32, its device status word; pass one zeroed once to reuse it). Rows of
     out and lse outside every sequence are left as they were.
     """
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    dev = q.device
-    qs = _tokens(q, "q", Hq, D, q.dtype)
-    ks = _tokens(k, "k", Hkv, D, q.dtype, T)
-    vs = _tokens(v, "v", Hkv, D, q.dtype, T)
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
-    with _on(dev):
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None else lse
-        status = torch.zeros(2, dtype=torch.int32, device=dev) if status is None else status
-        _need(out, "out", q.dtype, (T, Hq, D))
-        _need(lse, "lse", torch.float32, (T, Hq))
-        _need(status, "status", torch.int32, (2,))
-        _same_device(dev, (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens"), (out, "out"), (lse, "lse"), (status, "status"))
+    T, Hq, D = _three(q, "q")
+    Hkv, dt, i = _three(k, "k")[1], q.dtype, _cuda_index(q, "q")
+    code = dtype_code(dt)
+    qs, ks, vs = _tokens(q, "q", T, Hq, D, dt, i), _tokens(k, "k", T, Hkv, D, dt, i), _tokens(v, "v", T, Hkv, D, dt, i)
+    n = cu_seqlens.numel()
+    _plain(cu_seqlens, "cu_seqlens", torch.int32, (n,), i)
+    with _on(i, stream):
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        else:
+            _plain(out, "out", dt, (T, Hq, D), i)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        else:
+            _plain(lse, "lse", torch.float32, (T, Hq), i)
+        if status is None:
+            status = torch.zeros(2, dtype=torch.int32, device=q.device)
+        else:
+            _plain(status, "status", torch.int32, (2,), i)
         _check(lib().qe_prompt_attend(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_seqlens.data_ptr(),
-                                      cu_seqlens.numel() - 1, T, Hq, Hkv, D, dtype_code(q.dtype), out.data_ptr(),
-                                      lse.data_ptr(), status.data_ptr(), _raw(stream, dev)), "qe_prompt_attend")
+                                      n - 1, T, Hq, Hkv, D, code, out.data_ptr(), lse.data_ptr(), status.data_ptr(),
+                                      _raw(stream, i)), "qe_prompt_attend")
     return out, lse, status
 
 
@@ -664,21 +689,24 @@ def prompt_mass(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_seqlens:
                 stream=None):
     """The attention weight each prompt token collects (qe_prompt_mass), from prompt_attend's inputs
     and lse. Returns (mass [T][Hkv] float32, status)."""
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    dev = q.device
-    qs = _tokens(q, "q", Hq, D, q.dtype)
-    ks = _tokens(k, "k", Hkv, D, q.dtype, T)
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
-    _need(lse, "lse", torch.float32, (T, Hq))
-    with _on(dev):
-        mass = torch.empty((T, Hkv), dtype=torch.float32, device=dev) if mass is None else mass
-        status = torch.zeros(2, dtype=torch.int32, device=dev) if status is None else status
-        _need(mass, "mass", torch.float32, (T, Hkv))
-        _need(status, "status", torch.int32, (2,))
-        _same_device(dev, (k, "k"), (lse, "lse"), (cu_seqlens, "cu_seqlens"), (mass, "mass"), (status, "status"))
-        _check(lib().qe_prompt_mass(q.data_ptr(), k.data_ptr(), qs, ks, lse.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T,
-                                    Hq, Hkv, D, dtype_code(q.dtype), mass.data_ptr(), status.data_ptr(), _raw(stream, dev)),
+    T, Hq, D = _three(q, "q")
+    Hkv, dt, i = _three(k, "k")[1], q.dtype, _cuda_index(q, "q")
+    code = dtype_code(dt)
+    qs, ks = _tokens(q, "q", T, Hq, D, dt, i), _tokens(k, "k", T, Hkv, D, dt, i)
+    n = cu_seqlens.numel()
+    _plain(cu_seqlens, "cu_seqlens", torch.int32, (n,), i)
+    _plain(lse, "lse", torch.float32, (T, Hq), i)
+    with _on(i, stream):
+        if mass is None:
+            mass = torch.empty((T, Hkv), dtype=torch.float32, device=q.device)
+        else:
+            _plain(mass, "mass", torch.float32, (T, Hkv), i)
+        if status is None:
+            status = torch.zeros(2, dtype=torch.int32, device=q.device)
+        else:
+            _plain(status, "status", torch.int32, (2,), i)
+        _check(lib().qe_prompt_mass(q.data_ptr(), k.data_ptr(), qs, ks, lse.data_ptr(), cu_seqlens.data_ptr(), n - 1, T,
+                                    Hq, Hkv, D, code, mass.data_ptr(), status.data_ptr(), _raw(stream, i)),
                "qe_prompt_mass")
     return mass, status
 
@@ -701,6 +729,7 @@ class Int4Cache:
         n = self.units * self.max_pages
         self.pages = torch.zeros((n, 20 * D), dtype=torch.uint8, device=device)
         self.device = self.pages.device
+        self._index = _cuda_index(self.pages, "device")
         self.page_table = torch.arange(n, dtype=torch.int32, device=device).view(self.units, self.max_pages)
         self.counts = torch.zeros(self.units + B, dtype=torch.int32, device=device)
         self.lengths, self.seen = self.counts[:self.units], self.counts[self.units:]
@@ -710,6 +739,7 @@ class Int4Cache:
         self._scratch = {}
         self._c = QeInt4Cache(B, Hkv, D, self.max_pages, n, *(t.data_ptr() for t in (
             self.pages, self.page_table, self.lengths, self.seen, self.mass, self.pos, self.status)))
+        self._ref = C.byref(self._c)
 
     def status_word(self):
         """(code, detail) of the device status word; synchronises."""
@@ -719,40 +749,45 @@ class Int4Cache:
     def append(self, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, mass=None, stream=None):
         """Quantise new tokens k, v [T][Hkv][D] (tokens may be strided), sequence b's in rows
         cu_seqlens[b] .. cu_seqlens[b + 1] - 1, with the weights mass [T][Hkv] float32 (None: zeros)."""
-        T = k.shape[0]
-        ks = _tokens(k, "k", self.Hkv, self.D, k.dtype)
-        vs = _tokens(v, "v", self.Hkv, self.D, k.dtype, T)
-        _need(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,))
+        T, i, dt = _three(k, "k")[0], self._index, k.dtype
+        ks, vs = _tokens(k, "k", T, self.Hkv, self.D, dt, i), _tokens(v, "v", T, self.Hkv, self.D, dt, i)
+        _plain(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,), i)
         if mass is not None:
-            _need(mass, "mass", torch.float32, (T, self.Hkv))
-        _same_device(self.device, (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens"), (mass, "mass"))
-        with _on(self.device):
-            _check(lib().qe_int4_append(C.byref(self._c), k.data_ptr(), v.data_ptr(), ks, vs, cu_seqlens.data_ptr(), T,
-                                        dtype_code(k.dtype), None if mass is None else mass.data_ptr(), _raw(stream, self.device)),
+            _plain(mass, "mass", torch.float32, (T, self.Hkv), i)
+        with _on(i, stream):
+            _check(lib().qe_int4_append(self._ref, k.data_ptr(), v.data_ptr(), ks, vs, cu_seqlens.data_ptr(), T,
+                                        dtype_code(dt), None if mass is None else mass.data_ptr(), _raw(stream, i)),
                    "qe_int4_append")
 
     def read(self, cu_seqlens: torch.Tensor, T: int, first=None, dtype=torch.bfloat16, k_out=None, v_out=None,
              stream=None):
         """Values of entries first[u] + j of the units of sequence b in rows cu_seqlens[b] + j of
         (k_out, v_out) [T][Hkv][D]; rows without such an entry are left as they were."""
-        shape = (T, self.Hkv, self.D)
-        _need(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,))
+        shape, i = (T, self.Hkv, self.D), self._index
+        _plain(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,), i)
         if first is not None:
-            _need(first, "first", torch.int32, (self.units,))
-        with _on(self.device):
-            k_out = torch.empty(shape, dtype=dtype, device=self.device) if k_out is None else k_out
-            v_out = torch.empty(shape, dtype=dtype, device=self.device) if v_out is None else v_out
-            _need(k_out, "k_out", dtype, shape)
-            _need(v_out, "v_out", dtype, shape)
-            _same_device(self.device, (cu_seqlens, "cu_seqlens"), (first, "first"), (k_out, "k_out"), (v_out, "v_out"))
-            _check(lib().qe_int4_read(C.byref(self._c), cu_seqlens.data_ptr(), T, None if first is None else first.data_ptr(),
-                                      dtype_code(dtype), k_out.data_ptr(), v_out.data_ptr(), _raw(stream, self.device)), "qe_int4_read")
+            _plain(first, "first", torch.int32, (self.units,), i)
+        with _on(i, stream):
+            if k_out is None:
+                k_out = torch.empty(shape, dtype=dtype, device=self.device)
+            else:
+                _plain(k_out, "k_out", dtype, shape, i)
+            if v_out is None:
+                v_out = torch.empty(shape, dtype=dtype, device=self.device)
+            else:
+                _plain(v_out, "v_out", dtype, shape, i)
+            _check(lib().qe_int4_read(self._ref, cu_seqlens.data_ptr(), T, None if first is None else first.data_ptr(),
+                                      dtype_code(dtype), k_out.data_ptr(), v_out.data_ptr(), _raw(stream, i)),
+                   "qe_int4_read")
         return k_out, v_out
 
     def scratch(self, Hq: int) -> torch.Tensor:
-        """The scratch buffer that attend uses for this many query heads (made on first use)."""
+        """The scratch buffer that attend uses for this many query heads, made on first use: ask for it
+        before capturing a graph, whose memory pool it must not come from."""
         s = self._scratch.get(Hq)
         if s is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"call scratch({Hq}) before capturing attend")
             n = int(lib().qe_int4_scratch_bytes(self.B, Hq, self.Hkv, self.D, self.max_pages))
             if n == 0:
                 raise ValueError("unsupported shape")
@@ -762,24 +797,29 @@ class Int4Cache:
     def attend(self, q: torch.Tensor, out=None, accumulate: bool = True, scratch=None, stream=None) -> torch.Tensor:
         """One step's attention: q [B][Hq][D] (rows may be strided) over every live entry; returns out
         [B][Hq][D] in q's dtype. With accumulate the entries' weights grow by what they receive."""
-        B, Hq, D = q.shape
-        if B != self.B or D != self.D:
-            raise ValueError(f"q must be [{self.B}][Hq][{self.D}], got {tuple(q.shape)}")
-        qs = _tokens(q, "q", Hq, D, q.dtype)
-        with _on(self.device):
-            out = torch.empty((B, Hq, D), dtype=q.dtype, device=self.device) if out is None else out
-            _need(out, "out", q.dtype, (B, Hq, D))
-            scratch = self.scratch(Hq) if scratch is None else scratch
-            _same_device(self.device, (q, "q"), (out, "out"), (scratch, "scratch"))
-            _check(lib().qe_int4_attend(C.byref(self._c), q.data_ptr(), qs, Hq, dtype_code(q.dtype), int(accumulate),
-                                        out.data_ptr(), scratch.data_ptr(), scratch.numel(), _raw(stream, self.device)), "qe_int4_attend")
+        Hq, i, dt = _three(q, "q")[1], self._index, q.dtype
+        shape = (self.B, Hq, self.D)
+        qs = _tokens(q, "q", *shape, dt, i)
+        with _on(i, stream):
+            if out is None:
+                out = torch.empty(shape, dtype=dt, device=self.device)
+            else:
+                _plain(out, "out", dt, shape, i)
+            if scratch is None:
+                scratch = self.scratch(Hq)
+            elif scratch.get_device() != i or not scratch.is_contiguous():
+                raise ValueError(f"scratch must be a contiguous tensor on cuda:{i}")
+            _check(lib().qe_int4_attend(self._ref, q.data_ptr(), qs, Hq, dtype_code(dt), int(accumulate),
+                                        out.data_ptr(), scratch.data_ptr(), scratch.numel() * scratch.element_size(),
+                                        _raw(stream, i)), "qe_int4_attend")
         return out
 
     def evict(self, into: "Int4Cache", budget: int, recent: int, stream=None) -> "Int4Cache":
         """Copy each unit's `recent` newest entries and the heaviest others, `budget` in all, into
         another cache (its lengths, weights and positions are written; this one stays as it was)."""
-        _same_device(self.device, (into.pages, "into"))
-        with _on(self.device):
-            _check(lib().qe_int4_evict(C.byref(self._c), C.byref(into._c), budget, recent, _raw(stream, self.device)),
+        if into._index != self._index:
+            raise ValueError(f"the other cache is on {into.device}, expected {self.device}")
+        with _on(self._index, stream):
+            _check(lib().qe_int4_evict(self._ref, into._ref, budget, recent, _raw(stream, self._index)),
                    "qe_int4_evict")
         return into

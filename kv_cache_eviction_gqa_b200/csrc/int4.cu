@@ -287,13 +287,13 @@ struct SelShared {
   int wave[2][kSelWarps];       // per warp: entries equal to and above the threshold
   int count[2];                 // of this CTA
   uint32_t digit, above;
-  uint32_t keys[1];             // [this CTA's entries], when they fit
+  alignas(16) uint32_t keys[4]; // [this CTA's entries], when they fit
 };
 
 // The survivors of one unit, by a cluster of CTAs that hold consecutive parts of its entries: the
 // budget-th highest key T by a radix select whose histograms meet in distributed shared memory, the
-// entries above T, and of those equal to it the first ones. Their indices go, in order, to the pos
-// slots of their new places (the move kernel puts the positions there). The keys are read from global
+// entries above T, and of those equal to it the first ones. Where they lie (page and slot) goes, in
+// order, to the pos slots of their new places; the move kernel puts the positions there. The keys are read from global
 // memory once and kept in shared memory as far as they fit.
 __global__ void __launch_bounds__(kSelThreads) int4_select_kernel(Int4View s, Int4View d, int budget, int recent,
                                                                   int ctas, int cap) {
@@ -317,35 +317,67 @@ __global__ void __launch_bounds__(kSelThreads) int4_select_kernel(Int4View s, In
   const int p0 = (int)((long long)pages * rank / ctas), p1 = (int)((long long)pages * (rank + 1) / ctas);
   const int e0 = p0 * kInt4Page, mine = max(0, min(len, p1 * kInt4Page) - e0);
   const long long cut = (long long)s.seen[b] - recent;
-  const bool held = mine <= cap, all = len <= budget;
+  const bool held = mine <= cap;                   // else each pass reads them again
+  const bool all = len <= budget;
   auto global_key = [&](int x) -> uint32_t {       // of this CTA's entry x
     const int page = table[p0 + x / kInt4Page];
     if (page < 0 || page >= s.n_pages) return 0u;
     const size_t at = (size_t)page * kInt4Page + x % kInt4Page;
     return evict_key(s.mass[at], s.pos[at] >= cut);
   };
-  auto key_of = [&](int x) { return held ? sh.keys[x] : global_key(x); };
+  // the keys of entries x .. x + 3, x a multiple of 4 (what lies behind the last entry means nothing)
+  auto keys_of = [&](int x, uint32_t (&k)[4]) {
+    if (held) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sh.keys + x);
+      k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = x + j < mine ? global_key(x + j) : 0u;
+    }
+  };
+  auto place_of = [&](int x) -> int {              // page and slot, or -1
+    const int page = table[p0 + x / kInt4Page];
+    if (page >= 0 && page < s.n_pages) return page * kInt4Page + x % kInt4Page;
+    qe_record_error(s.status, QE_ERR_DEVICE_FAULT, u);
+    return -1;
+  };
   uint32_t T = 0;           // keys above T are kept,
   int ties = len;           // and the first `ties` equal to it
   if (!all) {
     for (int x = tid; x < kSelBins; x += kSelThreads) sh.hist[0][x] = sh.hist[1][x] = 0;
     __syncthreads();
-    // quarter pages: four entries a thread, all look-ups of a round in flight together
-    for (int q = tid; q < (p1 - p0) * 4; q += kSelThreads) {
-      const int page = table[p0 + q / 4];
-      const bool ok = page >= 0 && page < s.n_pages;
-      const size_t at = (size_t)(ok ? page : 0) * kInt4Page + (q % 4) * 4;
-      const float4 w = *reinterpret_cast<const float4*>(s.mass + at);
-      const int4 p = *reinterpret_cast<const int4*>(s.pos + at);
-      const uint32_t k[4] = {evict_key(w.x, p.x >= cut), evict_key(w.y, p.y >= cut), evict_key(w.z, p.z >= cut),
-                             evict_key(w.w, p.w >= cut)};
+    // quarter pages, four entries a thread; kBatch look-ups of a thread are in flight together
+    constexpr int kBatch = 4;
+    const int quarters = (p1 - p0) * 4;
+    for (int q0 = tid; q0 < quarters; q0 += kBatch * kSelThreads) {
+      int page[kBatch];
+      float4 w[kBatch];
+      int4 p[kBatch];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int x = q * 4 + j;
-        if (x >= mine) continue;
-        const uint32_t key = ok ? k[j] : 0u;
-        if (held) sh.keys[x] = key;
-        atomicAdd(&sh.hist[0][key >> 21], 1u);
+      for (int y = 0; y < kBatch; ++y) {
+        const int q = q0 + y * kSelThreads;
+        page[y] = q < quarters ? table[p0 + q / 4] : -1;
+      }
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y) {
+        const bool ok = page[y] >= 0 && page[y] < s.n_pages;
+        const size_t at = (size_t)(ok ? page[y] : 0) * kInt4Page + (tid % 4) * 4;
+        w[y] = *reinterpret_cast<const float4*>(s.mass + at);
+        p[y] = *reinterpret_cast<const int4*>(s.pos + at);
+        if (!ok) page[y] = -1;
+      }
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y) {
+        const uint32_t k[4] = {evict_key(w[y].x, p[y].x >= cut), evict_key(w[y].y, p[y].y >= cut),
+                               evict_key(w[y].z, p[y].z >= cut), evict_key(w[y].w, p[y].w >= cut)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int x = (q0 + y * kSelThreads) * 4 + j;
+          if (x >= mine) continue;
+          const uint32_t key = page[y] >= 0 ? k[j] : 0u;
+          if (held) sh.keys[x] = key;
+          atomicAdd(&sh.hist[0][key >> 21], 1u);
+        }
       }
     }
     uint32_t prefix = 0, mask = 0;
@@ -355,9 +387,12 @@ __global__ void __launch_bounds__(kSelThreads) int4_select_kernel(Int4View s, In
       const uint32_t bins = pass == 2 ? 1024u : 2048u;
       uint32_t* hist = sh.hist[pass & 1];
       if (pass > 0)
-        for (int x = tid; x < mine; x += kSelThreads) {
-          const uint32_t key = key_of(x);
-          if ((key & mask) == prefix) atomicAdd(&hist[key >> sft & (bins - 1)], 1u);
+        for (int x = tid * 4; x < mine; x += kSelThreads * 4) {
+          uint32_t k4[4];
+          keys_of(x, k4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((k4[j] & mask) == prefix && x + j < mine) atomicAdd(&hist[k4[j] >> sft & (bins - 1)], 1u);
         }
       if (ctas > 1) cluster_sync(); else __syncthreads();
       // thread i owns bins 2i, 2i + 1, the highest first
@@ -400,17 +435,30 @@ __global__ void __launch_bounds__(kSelThreads) int4_select_kernel(Int4View s, In
     T = prefix;
     ties = k;
   }
-  // order: each warp counts its consecutive entries, then writes them behind those before it
-  const int per = ((mine + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  // order: each warp counts its consecutive entries, equal to and above the threshold, then writes them
+  // behind those before it
+  const int per = ((mine + kSelWarps - 1) / kSelWarps + 127) & ~127;
   const int w0 = min(mine, warp * per), w1 = min(mine, w0 + per);
-  int neq = 0, ngt = 0;
-  for (int x0 = w0; x0 < w1; x0 += 32) {
-    const int x = x0 + lane;
-    const uint32_t key = all ? 0u : x < w1 ? key_of(x) : 0u;
-    neq += __popc(__ballot_sync(0xffffffffu, x < w1 && (all || key == T)));
-    ngt += __popc(__ballot_sync(0xffffffffu, x < w1 && !all && key > T));
+  auto flags = [&](int x, uint32_t& eq, uint32_t& gt) {   // bits of entries x .. x + 3
+    eq = gt = 0u;
+    if (x >= w1) return;
+    uint32_t k4[4] = {0u, 0u, 0u, 0u};
+    if (!all) keys_of(x, k4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = x + j < w1;
+      eq |= (in && k4[j] == T ? 1u : 0u) << j;
+      gt |= (in && k4[j] > T ? 1u : 0u) << j;
+    }
+  };
+  int n_eq = 0, n_gt = 0;
+  for (int x0 = w0; x0 < w1; x0 += 128) {
+    uint32_t eq, gt;
+    flags(x0 + lane * 4, eq, gt);
+    n_eq += __popc(eq), n_gt += __popc(gt);
   }
-  if (lane == 0) sh.wave[0][warp] = neq, sh.wave[1][warp] = ngt;
+  n_eq = __reduce_add_sync(0xffffffffu, n_eq), n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+  if (lane == 0) sh.wave[0][warp] = n_eq, sh.wave[1][warp] = n_gt;
   __syncthreads();
   if (warp < 2) {
     const int own = sh.wave[warp][lane];
@@ -424,25 +472,35 @@ __global__ void __launch_bounds__(kSelThreads) int4_select_kernel(Int4View s, In
     if (lane == 31) sh.count[warp] = inc;
   }
   if (ctas > 1) cluster_sync(); else __syncthreads();
-  neq = sh.wave[0][warp], ngt = sh.wave[1][warp];
+  int neq = sh.wave[0][warp], ngt = sh.wave[1][warp];
   for (int r = 0; r < rank; ++r) neq += (int)ld_peer(&sh.count[0], r), ngt += (int)ld_peer(&sh.count[1], r);
-  const uint32_t below = (1u << lane) - 1u;
-  for (int x0 = w0; x0 < w1; x0 += 32) {
-    const int x = x0 + lane;
-    const uint32_t key = all ? 0u : x < w1 ? key_of(x) : 0u;
-    const bool eq = x < w1 && (all || key == T), gt = x < w1 && !all && key > T;
-    const uint32_t beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
-    const int at_eq = neq + __popc(beq & below), at_gt = ngt + __popc(bgt & below);
-    if (gt || (eq && at_eq < ties)) {
-      const int to = at_gt + min(at_eq, ties);
-      const int page = dtable[to / kInt4Page];
-      if (page < 0 || page >= d.n_pages)
-        qe_record_error(d.status, QE_ERR_DEVICE_FAULT, u);
-      else
-        d.pos[(size_t)page * kInt4Page + to % kInt4Page] = e0 + x;
+  for (int x0 = w0; x0 < w1; x0 += 128) {
+    const int x = x0 + lane * 4;
+    uint32_t eq, gt;
+    flags(x, eq, gt);
+    const uint32_t own = __popc(eq) | __popc(gt) << 16;   // both counts of 128 entries in one word
+    uint32_t inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    neq += __popc(beq);
-    ngt += __popc(bgt);
+    int at_eq = neq + (int)((inc - own) & 0xffffu), at_gt = ngt + (int)((inc - own) >> 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool e = eq >> j & 1, g = gt >> j & 1;
+      if (g || (e && at_eq < ties)) {
+        const int to = at_gt + min(at_eq, ties);
+        const int page = dtable[to / kInt4Page];
+        if (page < 0 || page >= d.n_pages)
+          qe_record_error(d.status, QE_ERR_DEVICE_FAULT, u);
+        else
+          d.pos[(size_t)page * kInt4Page + to % kInt4Page] = place_of(x + j);
+      }
+      at_eq += e, at_gt += g;
+    }
+    const uint32_t tot = __shfl_sync(0xffffffffu, inc, 31);
+    neq += (int)(tot & 0xffffu), ngt += (int)(tot >> 16);
   }
   if (tid == 0 && rank == 0) d.lengths[u] = min(len, budget);
   if (ctas > 1) cluster_sync();            // no CTA leaves while another reads its counts
@@ -455,6 +513,7 @@ __global__ void __launch_bounds__(128) int4_move_kernel(Int4View s, Int4View d, 
   constexpr int NG = D / 32, RV = D / 32;   // 16-byte pieces of a row of codes
   const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int u = wid / pages_per_unit, p = wid % pages_per_unit;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched behind the selection, waits for it here
   if (u >= d.B * d.Hkv) return;
   const int live = min(kInt4Page, d.lengths[u] - p * kInt4Page);
   if (live <= 0) return;
@@ -464,16 +523,9 @@ __global__ void __launch_bounds__(128) int4_move_kernel(Int4View s, Int4View d, 
   int sp = -1, ss = 0;
   const size_t at = (size_t)dp * kInt4Page + lane;
   if (lane < live) {
-    const int e = d.pos[at];
-    const bool in = e >= 0 && e < s.max_pages * kInt4Page;   // holds unless tables share a page
-    sp = !in ? -1 : s.table[(size_t)u * s.max_pages + e / kInt4Page];
-    ss = e % kInt4Page;
-    if (sp < 0 || sp >= s.n_pages) {
-      qe_record_error(s.status, QE_ERR_DEVICE_FAULT, u);
-      sp = -1;
-    }
-    if (sp >= 0) {
-      const size_t from = (size_t)sp * kInt4Page + ss;
+    const int from = d.pos[at];
+    if (from >= 0 && from / kInt4Page < s.n_pages) {   // a bad page was recorded by the selection
+      sp = from / kInt4Page, ss = from % kInt4Page;
       d.mass[at] = s.mass[from];
       d.pos[at] = s.pos[from];
     }
@@ -536,7 +588,9 @@ int int4_view(const qe_int4_cache* c, Int4View* v) {
       !qe_aligned(c->mass, 16) || !qe_aligned(c->pos, 16))
     return QE_ERR_INVALID_ARG;
   if (c->D != 64 && c->D != 128) return QE_ERR_UNSUPPORTED_SHAPE;
-  if ((long long)c->B * c->Hkv * c->max_pages * kInt4Page >= (1ll << 31)) return QE_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)c->B * c->Hkv * c->max_pages * kInt4Page >= (1ll << 31) ||
+      (long long)c->n_pages * kInt4Page >= (1ll << 31))
+    return QE_ERR_UNSUPPORTED_SHAPE;
   *v = Int4View{static_cast<uint8_t*>(c->pages), c->page_table, c->lengths, c->seen, c->mass,
                 c->pos, c->status, c->B, c->Hkv, c->max_pages, c->n_pages};
   return QE_OK;
@@ -638,8 +692,13 @@ QE_API int qe_int4_evict(const qe_int4_cache* src, const qe_int4_cache* dst, int
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, int4_select_kernel, s, d, budget, recent, ctas, cap) != cudaSuccess) return QE_ERR_CUDA;
-  const int grid = (int)(((long long)U * ppu + 3) / 4);
-  if (src->D == 128) int4_move_kernel<128><<<grid, 128, 0, st>>>(s, d, ppu);
-  else int4_move_kernel<64><<<grid, 128, 0, st>>>(s, d, ppu);
+  cfg.gridDim = dim3((unsigned)(((long long)U * ppu + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  const cudaError_t moved = src->D == 128 ? cudaLaunchKernelEx(&cfg, int4_move_kernel<128>, s, d, ppu)
+                                          : cudaLaunchKernelEx(&cfg, int4_move_kernel<64>, s, d, ppu);
+  if (moved != cudaSuccess) return QE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QE_OK : QE_ERR_CUDA;
 }

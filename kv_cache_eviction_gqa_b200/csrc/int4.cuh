@@ -42,30 +42,33 @@ __device__ __forceinline__ float int4_inv15(uint32_t meta) {
 }
 
 // Codes of four elements, nibble by nibble: clamp(rint(f32(f32(x - z) / s)), 0, 15), 0 if s == 0, ties
-// to even. y = (x - z) / (15 s) saturated to [0, 1] (the clamp's bounds are integers, so it may
-// come first) times 15 is the quotient to 15 x 2^-20; adding 1.5 x 2^23 rounds it into the sum's low
-// bits. When one of the four lies within 2^-12 of a half-integer the correctly rounded division
-// decides, so the codes are those of the definition in every case.
+// to even, by correctly rounded division: the definition, rare enough to stay out of line.
+static __device__ __noinline__ uint32_t int4_codes_exact(float a, float b, float c, float d, uint32_t meta) {
+  const float s = int4_scale(meta), z = int4_zero(meta), x[4] = {a, b, c, d};
+  uint32_t n = 0u;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) n |= min(__float2uint_rn(__fdiv_rn(__fsub_rn(x[i], z), s)), 15u) << (4 * i);
+  return n;   // negative quotients and NaN convert to 0
+}
+// The same codes by y = (x - z) / (15 s) saturated to [0, 1] (the clamp's bounds are integers, so it
+// may come first): 15 y is within 4e-6 of the quotient, and adding 1.5 x 2^23 rounds it into the sum's
+// low bits. When one of the four lies within 2^-17 of a half-integer the definition decides.
 __device__ __forceinline__ uint32_t int4_codes(float a, float b, float c, float d, uint32_t meta, float inv15) {
   constexpr float kMagic = 12582912.f;   // 1.5 x 2^23: bits 0x4B400000
   const float z = int4_zero(meta), x[4] = {a, b, c, d};
-  float far = 0.f;
+  float off[4];
   uint32_t n = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float y = __saturatef(__fmul_rn(__fsub_rn(x[i], z), inv15));   // NaN gives 0
     const float t = __fmaf_rn(y, 15.f, kMagic);
-    far = fmaxf(far, fabsf(__fmaf_rn(y, 15.f, __fsub_rn(kMagic, t))));
+    off[i] = fabsf(__fmaf_rn(y, 15.f, __fsub_rn(kMagic, t)));
     n += __float_as_uint(t) << (4 * i);   // the constant's low 16 bits are 0
   }
-  n &= 0xffffu;
-  if (far > 0.5f - 0x1p-12f) {
-    const float s = int4_scale(meta);
-    n = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n |= min(__float2uint_rn(__fdiv_rn(__fsub_rn(x[i], z), s)), 15u) << (4 * i);
-  }
-  return n;
+  float far;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(far) : "f"(off[0]), "f"(off[1]), "f"(off[2]));
+  if (fmaxf(far, off[3]) > 0.5f - 0x1p-17f) return int4_codes_exact(a, b, c, d, meta);
+  return n & 0xffffu;
 }
 
 // device view of a qe_int4_cache

@@ -39,12 +39,13 @@ constexpr int kJoin = 32;           // partials that one join takes: a lane each
 constexpr int kGroup = 16;
 static_assert(kMaxCtas / kGroup + 2 <= kJoin, "the groups of one unit fit a join");
 constexpr int kMinPages = 8;        // weight of a range below which more CTAs only add merging
-// A unit weighs its pages and this many more, about what starting and merging a piece costs: without
-// it a CTA that drew a run of short units ended last by far (16 000 to 1 tokens a sequence, 64 units:
-// 65 us, 46 of them such a CTA's)
-constexpr int kUnitWeight = 8;
+// A unit weighs its pages and this many more, what a CTA loses on a second piece: without it a CTA that
+// drew a run of short units ended last by far (16 000 to 1 tokens a sequence, 64 units: 65 us, 46 of
+// them such a CTA's), and with 8 the CTAs that cross from one unit to the next, 26 us where the others
+// took 19 (a page is 0.2 us)
+constexpr int kUnitWeight = 24;
 constexpr int kThreads = kWarps * 32;
-constexpr int kWeighThreads = 256;  // of the second kernel, a quarter page each
+constexpr int kWeighThreads = 256, kWeighEach = 4;   // threads of the second kernel, entries of each
 
 struct AttendArgs {
   Int4View c;
@@ -69,6 +70,19 @@ __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// a bulk copy whose source is read once: it leaves L2 before the scores do
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void bulk_g2s_once(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
 }
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   uint32_t y;
@@ -150,24 +164,21 @@ __device__ __forceinline__ void join_parts(const float* ml, const float* po, int
     if (lane == 0) s_ml[0][h] = M, s_ml[1][h] = l;
   }
   __syncthreads();
-  for (int x = tid; x < G * D; x += kThreads) {
-    float acc = 0.f;
-    int y = 0;
-    for (; y + 8 <= n; y += 8) {
-      float v[8];
+  // a thread's elements side by side, so that all their loads of two partials are in flight together
+  constexpr int kMost = 8 * D / kThreads;
+  float acc[kMost];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __ldcg(po + (size_t)(y + j) * 8 * D + x);
+  for (int k = 0; k < kMost; ++k) acc[k] = 0.f;
+#pragma unroll 2
+  for (int y = 0; y < n; ++y)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc = fmaf(v[j], s_f[x / D][y + j], acc);
+    for (int k = 0; k < kMost; ++k) {
+      const int x = tid + k * kThreads;
+      if (x < G * D) acc[k] = fmaf(__ldcg(po + (size_t)y * 8 * D + x), s_f[x / D][y], acc[k]);
     }
-    float v[7];
 #pragma unroll
-    for (int j = 0; j < 7; ++j) v[j] = y + j < n ? __ldcg(po + (size_t)(y + j) * 8 * D + x) : 0.f;
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (y + j < n) acc = fmaf(v[j], s_f[x / D][y + j], acc);
-    put(x, acc);
-  }
+  for (int k = 0; k < kMost; ++k)
+    if (tid + k * kThreads < G * D) put(tid + k * kThreads, acc[k]);
 }
 
 template <typename T, int D>
@@ -227,6 +238,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
   if (p >= p_end) return;
   int u = s_unit, base = s_base;         // base: the place of the unit's first page
   uint32_t fills = 0;                    // copies this warp has waited for: stage and phase
+  const uint64_t once = read_once_policy();
   bool ok = true;
   int np = unit_pages(c, u);
   base += kUnitWeight;
@@ -259,8 +271,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
     auto issue = [&](int i, int pa, int pb) {   // lane 0
       const int s = (fills + i) % kStages;
       mbar_arrive_expect_tx(&bars[s], ((pa >= 0) + (pb >= 0)) * L::PAGE);
-      if (pa >= 0) bulk_g2s(ring + s * L::STAGE, c.pages + (size_t)pa * L::PAGE, L::PAGE, &bars[s]);
-      if (pb >= 0) bulk_g2s(ring + s * L::STAGE + L::PAGE, c.pages + (size_t)pb * L::PAGE, L::PAGE, &bars[s]);
+      if (pa >= 0) bulk_g2s_once(ring + s * L::STAGE, c.pages + (size_t)pa * L::PAGE, L::PAGE, &bars[s], once);
+      if (pb >= 0) bulk_g2s_once(ring + s * L::STAGE + L::PAGE, c.pages + (size_t)pb * L::PAGE, L::PAGE, &bars[s], once);
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
@@ -581,43 +593,48 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
   }
 }
 
-// The weights of a unit's entries from their scores: four entries, a quarter page, a thread. Launched
-// behind the kernel above without waiting for it to drain; it waits here. Bound by the scores' way
-// through L2 and the weights' through HBM.
+// The weights of a unit's entries from their scores, kWeighEach entries a thread, a block's width apart:
+// every load of a warp is one run, and a thread's are in flight together. Launched behind the kernel
+// above without waiting for it to drain; it waits here. Bound by the scores' way through L2 and the
+// weights' through HBM.
 __global__ void __launch_bounds__(kWeighThreads) int4_weigh_kernel(AttendArgs a) {
   const Int4View& c = a.c;
-  const int u = blockIdx.y, q = blockIdx.x * kWeighThreads + threadIdx.x, e = q * 4;
-  const int len = c.lengths[u];
-  const bool live = len >= 0 && (long long)len <= (long long)c.max_pages * kInt4Page && e < len;
-  const int page = live ? c.table[(size_t)u * c.max_pages + q / 4] : -1;
-  const bool has = page >= 0 && page < c.n_pages;  // a bad one was recorded by the first kernel
-  float* m = c.mass + (has ? (size_t)page * kInt4Page + e % kInt4Page : 0);
-  const float4 was = has ? *reinterpret_cast<const float4*>(m) : make_float4(0.f, 0.f, 0.f, 0.f);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!has) return;
-  const float* ml = a.unit_ml + u * 16;
-  const float* sc = a.scores + ((size_t)(a.prefix[u] + kUnitWeight) * kInt4Page + e) * a.GP;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int h = 0; h < a.G; h += 2) {
-    float2 s[4];
+  const int u = blockIdx.y, e0 = blockIdx.x * kWeighThreads * kWeighEach + threadIdx.x;
+  int len = c.lengths[u];
+  if (len < 0 || (long long)len > (long long)c.max_pages * kInt4Page) len = 0;
+  int page[kWeighEach];
+  float was[kWeighEach], w[kWeighEach];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = __ldcs(reinterpret_cast<const float2*>(sc + j * a.GP + h));
+  for (int j = 0; j < kWeighEach; ++j) {
+    const int e = e0 + j * kWeighThreads;
+    page[j] = e < len ? c.table[(size_t)u * c.max_pages + e / kInt4Page] : -1;
+    if (page[j] >= c.n_pages) page[j] = -1;        // a bad one was recorded by the first kernel
+  }
+#pragma unroll
+  for (int j = 0; j < kWeighEach; ++j) {
+    was[j] = page[j] >= 0 ? c.mass[(size_t)page[j] * kInt4Page + threadIdx.x % kInt4Page] : 0.f;
+    w[j] = 0.f;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float* ml = a.unit_ml + u * 16;
+  const float* sc = a.scores + ((size_t)(a.prefix[u] + kUnitWeight) * kInt4Page + e0) * a.GP;
+  for (int h = 0; h < a.G; h += 2) {
     const float m0 = ml[h] - 4.f, i0 = ml[8 + h];
     const bool pair = h + 1 < a.G;
     const float m1 = pair ? ml[h + 1] - 4.f : 0.f, i1 = pair ? ml[9 + h] : 0.f;
+    float2 s[kWeighEach];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kWeighEach; ++j)
+      s[j] = page[j] >= 0 ? *reinterpret_cast<const float2*>(sc + (size_t)j * kWeighThreads * a.GP + h) : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kWeighEach; ++j) {
       w[j] = fmaf(ex2f(s[j].x - m0), i0, w[j]);
       if (pair) w[j] = fmaf(ex2f(s[j].y - m1), i1, w[j]);
     }
   }
-  if (e + 4 <= len) {
-    *reinterpret_cast<float4*>(m) = make_float4(was.x + w[0], was.y + w[1], was.z + w[2], was.w + w[3]);
-  } else {                                         // slots behind the last entry stay as they were
-    m[0] = was.x + w[0];
-    if (e + 1 < len) m[1] = was.y + w[1];
-    if (e + 2 < len) m[2] = was.z + w[2];
-  }
+#pragma unroll
+  for (int j = 0; j < kWeighEach; ++j)
+    if (page[j] >= 0) c.mass[(size_t)page[j] * kInt4Page + threadIdx.x % kInt4Page] = was[j] + w[j];
 }
 
 struct ScratchLayout {
@@ -654,7 +671,8 @@ int launch(const AttendArgs& a, cudaStream_t st) {
   if (a.weigh) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
-    cfg.gridDim = dim3((a.c.max_pages * 4 + kWeighThreads - 1) / kWeighThreads, U);
+    constexpr int kPer = kWeighThreads * kWeighEach / kInt4Page;   // pages a block
+    cfg.gridDim = dim3((a.c.max_pages + kPer - 1) / kPer, U);
     cfg.blockDim = dim3(kWeighThreads);
     cfg.stream = st;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
