@@ -456,8 +456,8 @@ QE_API int qe_prompt_mass(const void* q, const void* k, long long q_stride, long
  *     length out of range, detail = the unit, which counts as empty; bounds out of order, detail =
  *     the sequence, nothing is done), QE_ERR_POOL_EXHAUSTED (an append that does not fit, detail =
  *     the unit, which stays as it was), QE_ERR_DEVICE_FAULT (a page-table entry outside [0, n_pages),
- *     detail = the unit; its entries count as absent), QE_ERR_TIMEOUT. The words from the third on
- *     are the library's own. One call at a time may use a cache. */
+ *     detail = the unit; its entries count as absent), QE_ERR_TIMEOUT (zero the whole array
+ *     before the next call). The words from the third on are the library's own. One call at a time may use a cache. */
 typedef struct {
   int B, Hkv, D;            /* sequences, kv heads, head dim (64 or 128)          */
   int max_pages;            /* entries of a unit's page-table row                 */

@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
     int st = fills % kStages;
     uint32_t ph = (fills / kStages) & 1;
 
-    for (int i = 0; i < mine; ++i) {
+    int i = 0;
+    for (; i < mine; ++i) {
       if (!__all_sync(0xffffffffu, mbar_try_wait(&bars[st], ph)))
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], ph, c.status, 6001));
       if (!ok) break;
@@ -500,8 +501,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
       }
       if (++st == kStages) st = 0, ph ^= 1;
     }
-    fills += mine > 0 ? mine : 0;
-    if (!ok) break;                      // the status word holds the reason
+    if (!ok) {                           // the status word holds the reason; no copy stays in flight
+      for (int x = i; x < min(mine, i + kStages); ++x)
+        mbar_wait_bounded(&bars[(fills + x) % kStages], ((fills + x) / kStages) & 1, c.status, 6002);
+      break;
+    }
+    fills += mine;
 
     // ---- merge the warps ----
 #pragma unroll

@@ -73,6 +73,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
@@ -308,6 +311,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     fence_mbar_init();
   }
   if (warp == kRoleWarps + 1) tmem_alloc(tmem_slot, kTmemAll);
+  if (threadIdx.x == kRoleWarps * 32) prefetch_map(&tmQ), prefetch_map(&tmK), prefetch_map(&tmV);
+  // rows that no query fills (128 - G PT of a tile)
+  for (int x = a.G * a.PT * 8 + threadIdx.x; x < kTileM * 8; x += kPromptThreads)
+    for (int b = 0; b < 2 * S::KB; ++b) *reinterpret_cast<uint4*>(sQ + b * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -397,6 +405,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (!ok) break;
       }
+      // no copy is in flight when the CTA leaves, even if a wait gave up
+      for (int x = max(0, ring - S::NS); x < ring; ++x) mbar_wait_bounded(&full[x % S::NS], (x / S::NS) & 1, a.status, 5021);
+      for (int t = 0; t < 2; ++t)
+        if (used[t] > 0) mbar_wait_bounded(&qfull[t], (used[t] - 1) & 1, a.status, 5021);
     } else if (warp == kRoleWarps + 1) {
       // ---- products ----
       const bool lead = lane == 0;
@@ -687,6 +699,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     fence_mbar_init();
   }
   if (warp == kRoleWarps + 1) tmem_alloc(tmem_slot, kTmemAll);
+  if (threadIdx.x == kRoleWarps * 32) prefetch_map(&tmQ), prefetch_map(&tmK);
   // rows that no query fills (128 - G PT of them): zero scores, which their -inf bias makes nothing of
   for (int x = a.G * a.PT * 8 + threadIdx.x; x < kTileM * 8; x += kPromptThreads)
     for (int b = 0; b < S::NS * S::KB; ++b) *reinterpret_cast<uint4*>(sQ + b * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
@@ -707,13 +720,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int t = 0; t < two; ++t)
         for (int kb = 0; kb < S::KB; ++kb)
           tma_load_3d(sK + t * S::TILE + kb * kBoxBytes, &tmK, kb * 64, kvh, start + key0 + t * kTileM, kfull);
-      for (int i = 0; i < N; ++i) {
+      int i = 0;
+      for (; i < N; ++i) {
         const int s = i % S::NS;
         if (!wait_or_abort(&empty[s], ((i / S::NS) & 1) ^ 1, abort_flag, a.status, 5101)) break;
         mbar_arrive_expect_tx(&full[s], S::KB * a.G * a.PT * 128);
         for (int kb = 0; kb < S::KB; ++kb)
           tma_load_3d(sQ + s * S::TILE + kb * kBoxBytes, &tmQ, kb * 64, kvh * a.G, start + (qt0 + i * ranks) * a.PT, &full[s]);
       }
+      // no copy is in flight when the CTA leaves, even if a wait gave up
+      for (int x = max(0, i - S::NS); x < i; ++x) mbar_wait_bounded(&full[x % S::NS], (x / S::NS) & 1, a.status, 5121);
+      mbar_wait_bounded(kfull, 0, a.status, 5121);
     }
   } else if (N > 0 && warp == kRoleWarps + 1) {
     if (lane == 0 && wait_or_abort(kfull, 0, abort_flag, a.status, 5102)) {

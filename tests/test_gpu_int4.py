@@ -470,3 +470,104 @@ def test_binding_refusals():
         c.evict(B.Int4Cache(1, 2, 64, 16), 17, 0)
     with pytest.raises(RuntimeError, match="invalid"):
         c.evict(B.Int4Cache(1, 1, 64, 16), 16, 0)
+
+
+# ---- large and unusual states ---------------------------------------------------------
+
+
+def test_attend_one_long_unit():
+    """One unit over every CTA: its partials are joined in two steps."""
+    c, *_ = _filled([50000], 1, 64, "fp16")
+    q = _draw(82, (1, 2, 64), "fp16")
+    before = c.mass.clone()
+    _check_attend(c, q, c.attend(q), before, "fp16")
+    assert not c.status[2:].any()                       # the tickets are back at 0
+
+
+def test_evict_more_entries_than_shared_memory_holds():
+    """450 000 entries of one unit: the selection reads them anew in every pass."""
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    n = 450000
+    c = Int4Cache(1, 1, 64, n)
+    _scatter(c, 4)
+    c.lengths.fill_(n)
+    c.seen.fill_(n)
+    g = torch.Generator().manual_seed(6)
+    at = torch.arange(n, device="cuda")
+    page = c.page_table[0].long()[at // 16]
+    mass = torch.randint(0, 5000, (n,), generator=g).float().cuda()                  # many ties
+    c.mass[page, at % 16] = mass
+    c.pos[page, at % 16] = at.int()
+    for budget, recent in ((1000, 10), (300000, 5000)):
+        d = Int4Cache(1, 1, 64, budget)
+        c.evict(d, budget, recent)
+        m = mass.clone()
+        m[n - recent:] = float("inf")
+        keep = torch.sort(m, descending=True, stable=True).indices[:budget].sort().values
+        e = torch.arange(budget, device="cuda")
+        assert torch.equal(d.pos.view(-1)[e], keep.int()) and torch.equal(d.mass.view(-1)[e], mass[keep])
+        assert d.lengths.item() == budget and c.status_word() == (0, 0) and d.status_word() == (0, 0)
+
+
+@pytest.mark.slow
+def test_pages_behind_four_gigabytes():
+    """A pool of 4.5 GB whose last pages are in use: every byte offset passes 32 bits."""
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    n_pages = 1760000
+    c = Int4Cache(1, 1, 128, 16 * n_pages)
+    assert c.pages.numel() > 1 << 32
+    c.page_table[0, :4] = torch.arange(n_pages - 1, n_pages - 5, -1, dtype=torch.int32)
+    k, v = _draw(1, (60, 1, 128), "bf16"), _draw(2, (60, 1, 128), "bf16")
+    c.append(k, v, _cu([60]))
+    kr, _ = c.read(_cu([60]), 60)
+    want = torch.from_numpy(P.int4_values(*P.int4_quantize(_np(k))).astype(np.float32)).bfloat16()
+    assert torch.equal(kr.cpu(), want) and not c.pages[:n_pages - 4].any()
+    q = _draw(3, (1, 2, 128), "bf16")
+    out = c.attend(q)
+    ref = Int4Cache(1, 1, 128, 64)
+    ref.append(k, v, _cu([60]))
+    assert torch.equal(out, ref.attend(q))
+    d = Int4Cache(1, 1, 128, 16)
+    c.evict(d, 10, 5)
+    e = Int4Cache(1, 1, 128, 16)
+    ref.evict(e, 10, 5)
+    assert torch.equal(d.pages, e.pages) and torch.equal(d.pos, e.pos) and torch.equal(d.mass, e.mass)
+
+
+def test_calls_on_a_given_stream():
+    """Every call on a stream that is not the current one, ordered by that stream alone."""
+    from kv_cache_eviction_gqa_b200.binding import Int4Cache
+    c, k, v, mass = _filled([300, 41], 2, 64, "bf16", room=8)
+    q = _draw(83, (2, 4, 64), "bf16")
+    ref, *_ = _filled([300, 41], 2, 64, "bf16", room=8)
+    ref.append(k[:2], v[:2], _cu([1, 1]))
+    want = ref.attend(q)
+    want_d = ref.evict(Int4Cache(2, 2, 64, 32), 32, 4)
+    d = Int4Cache(2, 2, 64, 32)
+    one = _cu([1, 1])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    c.append(k[:2], v[:2], one, stream=s)
+    out = c.attend(q, stream=s)
+    c.evict(d, 32, 4, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(d.pages, want_d.pages) and torch.equal(d.mass, want_d.mass)
+
+
+def test_scratch_is_asked_for_before_capture():
+    c, *_ = _filled([30], 1, 64, "bf16")
+    q, out = _draw(84, (1, 2, 64), "bf16"), torch.empty((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="before capturing"):
+        with torch.cuda.graph(g, stream=side):
+            out.zero_()
+            c.attend(q, out=out)
+    c.scratch(2)
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2, stream=side):
+        c.attend(q, out=out, accumulate=False)
+    g2.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, c.attend(q, accumulate=False))
