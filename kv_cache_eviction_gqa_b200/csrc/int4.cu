@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kRowThreads) int4_append_kernel(Int4View c, Ro
   __syncthreads();
   if (!s_ok) return;
   const int l = lane % LPI, g = l / 8, e8 = l % 8, half = lane / LPI;
+  const int k_at = ((e8 >> 1) * NG + g) * 4 + (e8 & 1) * 2, v_at = 8 * D + (e8 * NG + g) * 2;   // in a page's rows
   const int tiles = (a.T + TILE - 1) / TILE;
   const long long items = (long long)tiles * c.Hkv;
   for (long long it = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); it < items;
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(kRowThreads) int4_append_kernel(Int4View c, Ro
         vw[x] = __ldcs(reinterpret_cast<const uint2*>(vs + x * a.vs));
       }
     }
-    // lane r < TILE: where token t0 + r goes
-    int page = -1, slot = 0;
+    // lane r < TILE: where token t0 + r goes, page and slot in one number
+    int place = -1;
     if (lane < rows) {
       const int t = t0 + lane, b = sequence_of(a.cu, c.B, t);
       if (b >= 0) {                                       // else a row outside every sequence
@@ -123,15 +124,13 @@ __global__ void __launch_bounds__(kRowThreads) int4_append_kernel(Int4View c, Ro
           qe_record_error(c.status, len < 0 ? QE_ERR_INVALID_ARG : QE_ERR_POOL_EXHAUSTED, u);
         } else {
           const int e = len + t - s;
-          page = c.table[(size_t)u * c.max_pages + e / kInt4Page];
-          slot = e % kInt4Page;
+          const int page = c.table[(size_t)u * c.max_pages + e / kInt4Page];
           if (page < 0 || page >= c.n_pages) {
             qe_record_error(c.status, QE_ERR_DEVICE_FAULT, u);
-            page = -1;
           } else {
-            const size_t at = (size_t)page * kInt4Page + slot;
-            c.mass[at] = a.mass ? a.mass[(size_t)t * c.Hkv + h] : 0.f;
-            c.pos[at] = c.seen[b] + t - s;
+            place = page * kInt4Page + e % kInt4Page;
+            c.mass[place] = a.mass ? a.mass[(size_t)t * c.Hkv + h] : 0.f;
+            c.pos[place] = c.seen[b] + t - s;
           }
         }
       }
@@ -140,9 +139,9 @@ __global__ void __launch_bounds__(kRowThreads) int4_append_kernel(Int4View c, Ro
     const uint32_t km = int4_meta(-Elem<T>::hi(kr), Elem<T>::lo(kr)), vm = int4_meta(-Elem<T>::hi(vr), Elem<T>::lo(vr));
     const float ki = int4_inv15(km), vi = int4_inv15(vm);
     {                                                     // this lane's row and group: its four halves
-      const int pg_i = __shfl_sync(0xffffffffu, page, 8 * half + e8), i = __shfl_sync(0xffffffffu, slot, 8 * half + e8);
-      if (pg_i >= 0) {
-        uint16_t* m = reinterpret_cast<uint16_t*>(c.pages + (size_t)pg_i * (20 * D) + 16 * D);
+      const int at = __shfl_sync(0xffffffffu, place, 8 * half + e8), i = at & 15;
+      if (at >= 0) {
+        uint16_t* m = reinterpret_cast<uint16_t*>(c.pages + (size_t)(at >> 4) * (20 * D) + 16 * D);
         const int mk = i * NG + g, mv = ((((i & 7) >> 1) * NG + g) * 2 + (i >> 3)) * 2 + (i & 1);
         m[mk] = (uint16_t)km, m[D / 2 + mk] = (uint16_t)(km >> 16);
         m[D + mv] = (uint16_t)vm, m[3 * D / 2 + mv] = (uint16_t)(vm >> 16);
@@ -150,16 +149,16 @@ __global__ void __launch_bounds__(kRowThreads) int4_append_kernel(Int4View c, Ro
     }
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      const int pg_i = __shfl_sync(0xffffffffu, page, 8 * half + x), i = __shfl_sync(0xffffffffu, slot, 8 * half + x);
+      const int at = __shfl_sync(0xffffffffu, place, 8 * half + x);
       const int from = (lane & ~7) | x;
       const uint32_t mk = __shfl_sync(0xffffffffu, km, from), mv = __shfl_sync(0xffffffffu, vm, from);
       const float ik = __shfl_sync(0xffffffffu, ki, from), iv = __shfl_sync(0xffffffffu, vi, from);
       const uint32_t kc = int4_codes(Elem<T>::lo(kw[x].x), Elem<T>::hi(kw[x].x), Elem<T>::lo(kw[x].y), Elem<T>::hi(kw[x].y), mk, ik);
       const uint32_t vc = int4_codes(Elem<T>::lo(vw[x].x), Elem<T>::hi(vw[x].x), Elem<T>::lo(vw[x].y), Elem<T>::hi(vw[x].y), mv, iv);
-      if (pg_i < 0) continue;
-      uint8_t* pg = c.pages + (size_t)pg_i * (20 * D) + i * (D / 2);
-      *reinterpret_cast<uint16_t*>(pg + ((e8 >> 1) * NG + g) * 4 + (e8 & 1) * 2) = (uint16_t)kc;
-      *reinterpret_cast<uint16_t*>(pg + 8 * D + (e8 * NG + g) * 2) = (uint16_t)vc;
+      if (at < 0) continue;
+      uint8_t* pg = c.pages + (size_t)(at >> 4) * (20 * D) + (at & 15) * (D / 2);
+      *reinterpret_cast<uint16_t*>(pg + k_at) = (uint16_t)kc;
+      *reinterpret_cast<uint16_t*>(pg + v_at) = (uint16_t)vc;
     }
   }
   // the last CTA to finish moves the lengths on: every other one has read them

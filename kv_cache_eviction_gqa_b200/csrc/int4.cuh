@@ -41,34 +41,45 @@ __device__ __forceinline__ float int4_inv15(uint32_t meta) {
   return s == 0.f ? 0.f : r;
 }
 
-// Codes of four elements, nibble by nibble: clamp(rint(f32(f32(x - z) / s)), 0, 15), 0 if s == 0, ties
-// to even, by correctly rounded division: the definition, rare enough to stay out of line.
-static __device__ __noinline__ uint32_t int4_codes_exact(float a, float b, float c, float d, uint32_t meta) {
-  const float s = int4_scale(meta), z = int4_zero(meta), x[4] = {a, b, c, d};
-  uint32_t n = 0u;
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) n |= min(__float2uint_rn(__fdiv_rn(__fsub_rn(x[i], z), s)), 15u) << (4 * i);
-  return n;   // negative quotients and NaN convert to 0
+// y = (x - z) / (15 s) saturated to [0, 1], and how far 15 y is from the integer that adding 1.5 x 2^23
+// rounds it to; the sum's low bits are that integer
+constexpr float kInt4Magic = 12582912.f;   // 1.5 x 2^23: bits 0x4B400000
+constexpr float kInt4Near = 0.5f - 0x1p-17f;
+__device__ __forceinline__ float int4_round(float x, float z, float inv15, float* off) {
+  const float y = __saturatef(__fmul_rn(__fsub_rn(x, z), inv15));   // NaN gives 0
+  const float t = __fmaf_rn(y, 15.f, kInt4Magic);
+  *off = __fmaf_rn(y, 15.f, __fsub_rn(kInt4Magic, t));
+  return t;
 }
-// The same codes by y = (x - z) / (15 s) saturated to [0, 1] (the clamp's bounds are integers, so it
-// may come first): 15 y is within 4e-6 of the quotient, and adding 1.5 x 2^23 rounds it into the sum's
-// low bits. When one of the four lies within 2^-17 of a half-integer the definition decides.
+// The codes n of four elements with those next to a half-integer decided by correctly rounded division;
+// out of line (elements of few bits do fall on half-integers: 7 in 10 000 of normal bf16 values, so
+// every tenth warp comes here)
+static __device__ __noinline__ uint32_t int4_codes_near(float a, float b, float c, float d, uint32_t meta, float inv15,
+                                                        uint32_t n) {
+  const float s = int4_scale(meta), z = int4_zero(meta);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const float x = i == 0 ? a : i == 1 ? b : i == 2 ? c : d;
+    float off;
+    int4_round(x, z, inv15, &off);
+    if (fabsf(off) > kInt4Near)   // negative quotients convert to 0
+      n = (n & ~(15u << (4 * i))) | min(__float2uint_rn(__fdiv_rn(__fsub_rn(x, z), s)), 15u) << (4 * i);
+  }
+  return n;
+}
+// Codes of four elements, nibble by nibble: clamp(rint(f32(f32(x - z) / s)), 0, 15), 0 if s == 0, ties
+// to even. The clamp's bounds are integers, so it may come first; 15 y is within 4e-6 of the quotient,
+// and within 2^-17 of a half-integer the division decides, so the codes are the definition's in every case.
 __device__ __forceinline__ uint32_t int4_codes(float a, float b, float c, float d, uint32_t meta, float inv15) {
-  constexpr float kMagic = 12582912.f;   // 1.5 x 2^23: bits 0x4B400000
   const float z = int4_zero(meta), x[4] = {a, b, c, d};
   float off[4];
   uint32_t n = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float y = __saturatef(__fmul_rn(__fsub_rn(x[i], z), inv15));   // NaN gives 0
-    const float t = __fmaf_rn(y, 15.f, kMagic);
-    off[i] = fabsf(__fmaf_rn(y, 15.f, __fsub_rn(kMagic, t)));
-    n += __float_as_uint(t) << (4 * i);   // the constant's low 16 bits are 0
-  }
-  float far;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(far) : "f"(off[0]), "f"(off[1]), "f"(off[2]));
-  if (fmaxf(far, off[3]) > 0.5f - 0x1p-17f) return int4_codes_exact(a, b, c, d, meta);
-  return n & 0xffffu;
+  for (int i = 0; i < 4; ++i)   // the constant's low 16 bits are 0
+    n += __float_as_uint(int4_round(x[i], z, inv15, &off[i])) << (4 * i);
+  n &= 0xffffu;
+  const float far = fmaxf(fmaxf(fabsf(off[0]), fabsf(off[1])), fmaxf(fabsf(off[2]), fabsf(off[3])));
+  return far > kInt4Near ? int4_codes_near(a, b, c, d, meta, inv15, n) : n;
 }
 
 // device view of a qe_int4_cache
