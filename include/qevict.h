@@ -432,7 +432,7 @@ QE_API int qe_sekv_attend(const void* q, const void* K, const void* V, int B, in
  *     exp(q_i . k_j / sqrt(D) - lse_i).
  * Errors (returned, nothing launched): QE_ERR_INVALID_ARG (null or misaligned pointer, a bad stride,
  * B < 1, T < 0, Hq not a multiple of Hkv, bad dtype), QE_ERR_UNSUPPORTED_SHAPE (D not in {64, 128},
- * Hq / Hkv > 8, T > 2^30). T == 0 does nothing. Asynchronous on `stream`; allocates nothing. */
+ * Hq / Hkv > 8, T > 2^30 or (T / 32 + B) * Hkv >= 2^30). T == 0 does nothing. Asynchronous on `stream`; allocates nothing. */
 QE_API int qe_prompt_attend(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
                             long long v_stride, const int32_t* cu_seqlens, int B, int T, int Hq, int Hkv, int D,
                             int dtype, void* out, float* lse, int32_t* status, qe_stream_t stream);

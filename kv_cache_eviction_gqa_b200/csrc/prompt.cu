@@ -312,6 +312,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   if (warp == kRoleWarps + 1) tmem_alloc(tmem_slot, kTmemAll);
   if (threadIdx.x == kRoleWarps * 32) prefetch_map(&tmQ), prefetch_map(&tmK), prefetch_map(&tmV);
+  const int G = gridDim.x;
+  TileRef first{0, 0, 0};                // found while the barriers are set up
+  if (warp == kRoleWarps + 2) first = find_tile(a, 2 * a.PT, blockIdx.x / a.Hkv, false);
   // rows that no query fills (128 - G PT of a tile)
   for (int x = a.G * a.PT * 8 + threadIdx.x; x < kTileM * 8; x += kPromptThreads)
     for (int b = 0; b < 2 * S::KB; ++b) *reinterpret_cast<uint4*>(sQ + b * kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
@@ -334,9 +337,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (warp == kRoleWarps + 2) {
       // ---- items ----
       for (int j = 0;; ++j) {
-        const int G = gridDim.x, c = blockIdx.x, s = j % kItems;
+        const int c = blockIdx.x, s = j % kItems;
         const int item = j * G + (j & 1 ? G - 1 - c : c);
-        const TileRef t = find_tile(a, 2 * a.PT, item / a.Hkv, false);
+        const TileRef t = j == 0 ? first : find_tile(a, 2 * a.PT, item / a.Hkv, false);
         if (!__all_sync(0xffffffffu, wait(&iempty[s], (j / kItems) ^ 1, 5011))) break;
         if (lane == 0) {
           sItem[s] = ItemRef{t.start, t.len, t.tile * 2 * a.PT, item % a.Hkv};
@@ -919,7 +922,7 @@ int launch_mass(const void* q, const void* k, long long qs, long long ks, Prompt
   CUtensorMap tmQ, tmK;
   if ((e = make_map3(&tmQ, q, BF16, D, a.Hq, a.T, qs, a.G, a.PT))) return e;
   if ((e = make_map3(&tmK, k, BF16, D, a.Hkv, a.T, ks, 1, kTileM))) return e;
-  const int items = (a.T / (2 * kTileM) + (a.B < a.T ? a.B : a.T)) * a.Hkv;
+  const long long items = ((long long)a.T / (2 * kTileM) + (a.B < a.T ? a.B : a.T)) * a.Hkv;
   // One and a half items an SM and more balance by themselves, longest first (four prompts of 2048, 8 kv
   // heads: 94 us with one CTA an item, 107 with two); below that the longest alone would decide (8192
   // positions, 2 kv heads of 8: 949 us with one, 167 with four; a cluster of eight starts late: 206).
@@ -927,7 +930,7 @@ int launch_mass(const void* q, const void* k, long long qs, long long ks, Prompt
   while (ranks < 4 && 2 * items * ranks < 3 * sms_of[dev]) ranks *= 2;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3((unsigned)items * ranks);
+  cfg.gridDim = dim3((unsigned)(items * ranks));
   cfg.blockDim = dim3(kPromptThreads);
   cfg.dynamicSmemBytes = S::BYTES;
   cfg.stream = st;
