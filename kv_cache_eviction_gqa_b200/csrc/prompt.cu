@@ -608,9 +608,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const float inv = 1.f / l;
-      const bool mine = r < a.G * a.PT && pos < it.len;
-      const size_t row = (size_t)(it.start + pos) * a.Hq + it.kvh * a.G + r % a.G;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * D * 2 + half * D);
+      // the row's place behind the item's first one, or -1
+      const int place = r < a.G * a.PT && pos < it.len ? (pos - it.pos0) * a.Hq + r % a.G : -1;
+      const size_t row0 = (size_t)(it.start + it.pos0) * a.Hq + it.kvh * a.G;
       uint32_t o[D / 2];
 #pragma unroll
       for (int x = 0; x < D / 64; ++x) tmem_ld_x32(tO + 32 * x, o + 32 * x);
@@ -626,10 +626,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         else
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[x / 2]) : "f"(hi), "f"(lo));
       }
-      if (mine) {
+      if (place >= 0 && a.lse && half == 0) a.lse[row0 + place] = (m * a.c + log2f(l)) * 0.693147180559945309f;
+      // A thread has NC 16-byte pieces of its own row; NC lanes turn them about, so that each store writes
+      // whole runs (a row a lane, the stores alone took 2 us an item)
+      constexpr int NC = D / 16;
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-        if (a.lse && half == 0) a.lse[row] = (m * a.c + log2f(l)) * 0.693147180559945309f;
+      for (int s = NC / 2; s; s >>= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+          if (!(k & s))
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t in = __shfl_xor_sync(0xffffffffu, up ? o[4 * k + w] : o[4 * (k + s) + w], s);
+              if (up) o[4 * k + w] = in; else o[4 * (k + s) + w] = in;
+            }
+      }
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {       // piece lane % NC of the row of lane k of this group
+        const int at = __shfl_sync(0xffffffffu, place, (lane & ~(NC - 1)) + k);
+        if (at >= 0)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (row0 + at) * (D * 2) + half * D + (lane & (NC - 1)) * 16) =
+              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
     }
   }
