@@ -485,18 +485,25 @@ __global__ void __launch_bounds__(kSelThreads) int4_select_kernel(Int4View s, In
       if (lane >= o) inc += y;
     }
     int at_eq = neq + (int)((inc - own) & 0xffffu), at_gt = ngt + (int)((inc - own) >> 16);
+    int to[4], page[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool e = eq >> j & 1, g = gt >> j & 1;
-      if (g || (e && at_eq < ties)) {
-        const int to = at_gt + min(at_eq, ties);
-        const int page = dtable[to / kInt4Page];
-        if (page < 0 || page >= d.n_pages)
-          qe_record_error(d.status, QE_ERR_DEVICE_FAULT, u);
-        else
-          d.pos[(size_t)page * kInt4Page + to % kInt4Page] = place_of(x + j);
-      }
+      to[j] = g || (e && at_eq < ties) ? at_gt + min(at_eq, ties) : -1;
       at_eq += e, at_gt += g;
+    }
+    // the look-ups of four entries (all of one page) side by side
+    const bool any = (to[0] & to[1] & to[2] & to[3]) >= 0;
+    const int from = any ? place_of(x) : -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) page[j] = to[j] >= 0 ? dtable[to[j] / kInt4Page] : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (to[j] < 0) continue;
+      if (page[j] < 0 || page[j] >= d.n_pages)
+        qe_record_error(d.status, QE_ERR_DEVICE_FAULT, u);
+      else
+        d.pos[(size_t)page[j] * kInt4Page + to[j] % kInt4Page] = from < 0 ? -1 : from + j;
     }
     const uint32_t tot = __shfl_sync(0xffffffffu, inc, 31);
     neq += (int)(tot & 0xffffu), ngt += (int)(tot >> 16);
