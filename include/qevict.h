@@ -424,8 +424,8 @@ QE_API int qe_sekv_attend(const void* q, const void* K, const void* V, int B, in
  *   out [dev]: [T][Hq][D] dtype, o_i = sum_{j <= i} p_ij v_j. The weights are rounded once to dtype for
  *     the product; scores, maxima and sums are float32.
  *   lse [dev, float, may be NULL]: [T][Hq] ln sum_{j <= i} exp(q_i . k_j / sqrt(D)).
- *   The elements of a sequence's k and v must be finite (a row of v that is not reaches the outputs of
- *   up to 127 positions before it).
+ *   The outputs overlap no input. The elements of a sequence's k and v must be finite (a row of v that
+ *   is not reaches the outputs of up to 127 positions before it).
  * qe_prompt_mass: the weight each prompt token collects ("Resumo Técnico: QEvict", Pontuação
  *   Cumulativa, over the prompt's own queries), from qe_prompt_attend's lse:
  *   mass [dev, float]: [T][Hkv], mass_j = sum over the kv head's query heads and i >= j of
@@ -508,7 +508,7 @@ QE_API int qe_int4_attend(const qe_int4_cache* cache, const void* q, long long q
  *   src, dst: equal B, Hkv and D; no buffer of dst but its page_table and status may be one of src's;
  *     dst holds at least `budget` entries a unit.
  * All qe_int4_* errors (returned, nothing launched): QE_ERR_INVALID_ARG (null or misaligned pointer, bad
- * sizes or strides, budget < 1 or above dst's capacity, recent < 0, shared buffers),
+ * sizes or strides, budget < 1 or above dst's capacity, recent < 0 or above budget, shared buffers),
  * QE_ERR_UNSUPPORTED_SHAPE (D not in {64, 128}, B * Hkv * max_pages * 16 or n_pages * 16 >= 2^31). T == 0
  * does nothing.
  * Asynchronous on `stream`; allocates nothing. */

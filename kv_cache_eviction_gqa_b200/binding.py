@@ -815,8 +815,9 @@ class Int4Cache:
         return out
 
     def evict(self, into: "Int4Cache", budget: int, recent: int, stream=None) -> "Int4Cache":
-        """Copy each unit's `recent` newest entries and the heaviest others, `budget` in all, into
-        another cache (its lengths, weights and positions are written; this one stays as it was)."""
+        """Copy each unit's `recent` newest entries and the heaviest others, `budget` in all (at least
+        `recent`), into another cache (its lengths, weights and positions are written; this one stays as
+        it was)."""
         if into._index != self._index:
             raise ValueError(f"the other cache is on {into.device}, expected {self.device}")
         with _on(self._index, stream):

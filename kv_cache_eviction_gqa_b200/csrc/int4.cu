@@ -663,7 +663,8 @@ QE_API int qe_int4_evict(const qe_int4_cache* src, const qe_int4_cache* dst, int
   int e = int4_view(src, &s);
   if (e || (e = int4_view(dst, &d))) return e;
   if (src->B != dst->B || src->Hkv != dst->Hkv || src->D != dst->D) return QE_ERR_INVALID_ARG;
-  if (budget < 1 || recent < 0 || budget > (long long)d.max_pages * kInt4Page) return QE_ERR_INVALID_ARG;
+  if (budget < 1 || recent < 0 || recent > budget || budget > (long long)d.max_pages * kInt4Page)
+    return QE_ERR_INVALID_ARG;
   if (s.pages == d.pages || s.lengths == d.lengths || s.seen == d.seen || s.mass == d.mass || s.pos == d.pos)
     return QE_ERR_INVALID_ARG;
   const int U = s.B * s.Hkv, ppu = (budget + kInt4Page - 1) / kInt4Page;

@@ -166,3 +166,9 @@ def test_int4_call_refusals(L):
     assert L.qe_int4_evict(r(c), r(c), 8, 0, None) == -1
     assert L.qe_int4_evict(r(c), r(_cache(pages=2 * FAKE, lengths=2 * FAKE, mass=2 * FAKE, pos=2 * FAKE)), 8, 0, None) == -1
     assert L.qe_int4_evict(r(c), r(_cache(D=64, pages=2 * FAKE)), 8, 0, None) == -1
+
+
+def test_int4_evict_refuses_more_newest_than_the_budget(L):
+    """Which of the newest entries to drop is not defined."""
+    c, d = _cache(), _cache(pages=2 * FAKE, lengths=2 * FAKE, seen=2 * FAKE, mass=2 * FAKE, pos=2 * FAKE)
+    assert L.qe_int4_evict(C.byref(c), C.byref(d), 8, 9, None) == -1
