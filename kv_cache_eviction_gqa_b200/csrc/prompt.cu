@@ -51,10 +51,11 @@ __device__ __forceinline__ float ex2f(float x) {
 // 2^x of two arguments without the special-function unit: x = n + f with
 // n the nearest integer, taken by adding 1.5 x 2^23, and a polynomial of degree 5 in f in [-1/2, 1/2]
 // (least maximal relative error, fitted by iteratively reweighted least squares: 7.5e-8, 2.1e-7 evaluated in
-// float32; ex2.approx has 2e-7); n is added to the exponent. Arguments from -127 up to 8.
+// float32; ex2.approx has 2e-7), times 2^n. Arguments below 127; -127 and less give 0, NaN stays NaN.
 __device__ __forceinline__ float2 ex2_poly(float2 x) {
   constexpr float kMagic = 12582912.f;
-  x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.f));
   const float2 t = __fadd2_rn(x, make_float2(kMagic, kMagic));
   const float2 f = __fadd2_rn(x, __fadd2_rn(make_float2(kMagic, kMagic), make_float2(-t.x, -t.y)));
   float2 p = make_float2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
@@ -64,8 +65,8 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
   step(2.4022120237350464e-1f);
   step(6.931469440460205e-1f);
   step(1.0000001192092896f);
-  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+  return __fmul2_rn(p, make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                                   __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000)));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;

@@ -218,3 +218,27 @@ def test_long_prompt_sampled_rows():
         w = torch.exp(q[i:].double().flatten(0, 1) @ kd[i] / D ** 0.5 - lse[i:].double().flatten()).sum()
         assert abs(mass[i, 0].item() - w.item()) <= (ep + 2.0 ** -18) * w.item()
     assert abs(mass.double().sum().item() - 4 * n) <= 4 * n * 2.0 ** -12
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_query_shows_in_every_weight_it_gives(bad):
+    """Sixteen sequences, each with one query row that is not finite, at every place of a run of 16 columns:
+    its output and the weights of all keys it sees are NaN, nothing else is."""
+    from kv_cache_eviction_gqa_b200 import binding as B
+    n, Hq, Hkv, D = 600, 4, 2, 64
+    x = _draw(17, 16 * n, Hq, Hkv, D, "bf16")
+    rows = [b * n + 484 + b for b in range(16)]
+    x[rows, 1] = bad                                     # of kv head 0
+    x = x.cuda()
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    cu = _cu([n] * 16).cuda()
+    out, lse, status = B.prompt_attend(q, k, v, cu)
+    mass, _ = B.prompt_mass(q, k, lse, cu)
+    assert status.tolist() == [0, 0]
+    hit = torch.zeros((16 * n, Hq), dtype=torch.bool)
+    hit[rows, 1] = True
+    assert torch.equal(out.isnan().all(-1).cpu(), hit) and torch.equal(out.isnan().any(-1).cpu(), hit)
+    want = torch.zeros((16 * n, Hkv), dtype=torch.bool)
+    for b, i in enumerate(rows):
+        want[b * n:i + 1, 0] = True
+    assert torch.equal(mass.isnan().cpu(), want)
