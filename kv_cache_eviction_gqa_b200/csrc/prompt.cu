@@ -237,7 +237,7 @@ __device__ TileRef find_tile(const PromptArgs& a, int P, int rank, bool from_end
 //                   so that warp 17 has one wait a tile.
 // The roles pass items on through a ring, so the next item's loads and first products run while the
 // softmax warps still write the last one out (four prompts of 2048, 32/8 heads: 197 us with a CTA an
-// item, 157 us this way).
+// item, 150 us this way).
 // What bounds it: a tile's way round, some 3500 cycles, of which the tensor pipe has 1024 for either tile:
 // reading and searching the scores takes 400, the weights 1500 (1024 of them exponentials at the
 // special-function unit's rate; moving some to a polynomial gained nothing), P V and the next scores
@@ -504,11 +504,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t tS = lane_addr + t * kTileM, tO = lane_addr + 2 * kTileM + t * kTileM + half * (D / 2);
     float* own_x = sRow + (t * 2 + half) * kTileM + r;            // what the two halves of a row exchange
     const float* other_x = sRow + (t * 2 + (half ^ 1)) * kTileM + r;
-    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + q) : "memory"); };
+    // The warps of the two halves meet without a limit, so a warp that gives up arrives once more as it leaves;
+    // its partner finds the flag set behind that meeting and does not come to another one.
+    int gone = 0;
+    auto meet = [&]() {
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + q) : "memory");
+      gone = *abort_flag;
+    };
     int ring = 0, blocks = 0, used = 0;  // tiles through the ring, blocks and items of this group, before the item
     int side = 0;                        // exchanges alternate between two buffers: one is read when the other is written
     bool ok = true;
-    auto all = [&](uint64_t* bar, uint32_t parity, int where) { return __all_sync(0xffffffffu, wait(bar, parity, where)); };
+    auto all = [&](uint64_t* bar, uint32_t parity, int where) {
+      return __all_sync(0xffffffffu, !gone && wait(bar, parity, where));
+    };
     for (int j = 0; ok; ++j) {
       const int slot = j % kItems;
       ok = all(&ifull[slot], j / kItems, 5017);
@@ -596,6 +604,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (lane == 0) mbar_arrive(vclean);
         }
       }
+      ok = __all_sync(0xffffffffu, ok && !gone);
       if (!ok) break;
       ring += 2 * N;
       blocks += n;
@@ -651,6 +660,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
     }
+    if (!ok) asm volatile("bar.arrive %0, 64;" ::"r"(1 + t * 4 + q) : "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -697,7 +707,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* empty = full + S::NS;                                         // [NS]
   uint64_t* sfull = empty + S::NS;                                        // [2 tiles][2]
   uint64_t* sfree = sfull + 4;                                            // [2 tiles][2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sfree + 4);
+  uint64_t* drain = sfree + 4;                                            // every product done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* sTile = reinterpret_cast<int*>(tmem_slot + 2);                     // [3]
 
@@ -709,6 +720,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   if (threadIdx.x == 32) {
     mbar_init(kfull, 1);
+    mbar_init(drain, 1);
     for (int s = 0; s < S::NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -774,6 +786,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (i + S::NS < N) mma_commit(&empty[s]);
       }
+      if (!ok) {                         // products in flight, and what their commits announce, land first
+        mma_commit(drain);
+        mbar_wait_bounded(drain, 0, a.status, 5122);
+      }
     }
   } else if (N > 0 && warp < kRoleWarps) {
     const int grp = warp >> 2, t = grp >> 1, b = grp & 1, q = warp & 3, r = q * 32 + lane;
@@ -795,12 +811,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // whole at 16 000 positions, this one by the scores' own error).
     float total = 0.f, carry = 0.f;
     const float2 c2 = make_float2(a.c, a.c);
+    // The warps of a group meet without a limit, so one that gives up arrives once more as it leaves, and the
+    // others find the flag set behind that meeting.
+    bool ok = true;
     for (int i = b; t < two && i < N; i += 2) {        // every other query tile: those of this buffer
       float* nl = gL + (i >> 1 & 1) * kTileM;
       nl[gr] = next;
       if (i + 2 < N) next = fetch(i + 2);
       asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
-      if (!__all_sync(0xffffffffu, wait_or_abort(&sfull[2 * t + b], (i >> 1) & 1, abort_flag, a.status, 5105))) break;
+      ok = __all_sync(0xffffffffu,
+                      !*abort_flag && wait_or_abort(&sfull[2 * t + b], (i >> 1) & 1, abort_flag, a.status, 5105));
+      if (!ok) break;
       tc_fence_after();
       const int p0 = (qt0 + i * ranks) * a.PT;
       const bool open = p0 >= key0 + (t + 1) * kTileM - 1 && p0 + a.PT <= len;
@@ -848,6 +869,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       carry = __fsub_rn(__fsub_rn(sum, total), y);
       total = sum;
     }
+    if (!ok) asm volatile("bar.arrive %0, 128;" ::"r"(1 + grp) : "memory");
     sSum[grp * kTileM + r] = total;
   }
   __syncwarp();
