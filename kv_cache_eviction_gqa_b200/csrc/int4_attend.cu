@@ -10,9 +10,11 @@
 //              scaled by its row's s_ig in float32, and one m16n8k8 for all zeros (the sum of q
 //              over a group split into two fp16 parts);
 //     output   O_dh = sum_i c_id (s_ig p_ih) + sum_i z_ig p_ih:  the scale goes onto the weights.
-// q is scaled per head by a power of two into fp16's range. The weights are rounded to fp16 (times
-// 16, times s once more): 2^-11 relative, below the output's own rounding in bf16 and equal to it
-// in fp16; their sums, the maxima and the scores are float32.
+// q is scaled per head by a power of two into fp16's range. For the products the weights are rounded to
+// fp16 (times 16, times s once more). That is 2^-11 of c s each time, which may be several times the
+// element c s + z: still below the output's own rounding in bf16, but two to three times it in fp16.
+// So for fp16 a second product adds what either rounding left (8 x 32 768 entries: 80 instead of 72 us; error
+// 1.0 to 1.1 times that of rounding alone, before 1.8 and more). Sums, maxima and scores are float32.
 //
 // Split: the pages of all units, each unit led by the weight of starting it, form one flat list that is
 // cut into equal ranges, one a CTA, so batches of very different lengths load every SM alike. Warp w of a CTA takes every 4th pair of pages of
@@ -21,6 +23,8 @@
 // its partials, always in the same order. The scores of a weighing call go to scratch (float32, mostly
 // L2) and a second kernel turns them into weights once the unit's maximum and sum are known.
 #include <math.h>
+
+#include <type_traits>
 
 #include "int4.cuh"
 #include "warp_mma.cuh"
@@ -92,6 +96,11 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t y;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -185,6 +194,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(AttendArgs a) {
   using L = AttendLayout<D>;
   constexpr int NG = D / 32;
+  constexpr bool kFine = std::is_same<T, __half>::value;   // weights in two parts
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_sum[kWarps], s_unit, s_base, s_last;
   __shared__ float s_m[kWarps][8], s_l[kWarps][8], s_z[kWarps][8][NG];
@@ -438,13 +448,18 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
       }
       // 16 p: the factor cancels in the output and keeps p s clear of fp16's subnormals
       const float b0 = m0 - 4.f, b1 = m1 - 4.f;
-      uint32_t pb[kPair][2];
+      uint32_t pb[kPair][2], pl[kPair][2];
 #pragma unroll
       for (int y = 0; y < kPair; ++y) {
         const float p00 = ex2f(sc[y][0] - b0), p01 = ex2f(sc[y][1] - b1);
         const float p10 = ex2f(sc[y][2] - b0), p11 = ex2f(sc[y][3] - b1);
         l0 += p00 + p10, l1 += p01 + p11;
-        pb[y][0] = movm_t(pack_h2(p00, p01)), pb[y][1] = movm_t(pack_h2(p10, p11));
+        const uint32_t w0 = pack_h2(p00, p01), w1 = pack_h2(p10, p11);
+        pb[y][0] = movm_t(w0), pb[y][1] = movm_t(w1);
+        if constexpr (kFine) {
+          pl[y][0] = movm_t(pack_h2(p00 - h_lo(w0), p01 - h_hi(w0)));
+          pl[y][1] = movm_t(pack_h2(p10 - h_lo(w1), p11 - h_hi(w1)));
+        }
       }
       // ---- output: rows are elements, the contraction runs over a page's 16 entries ----
 #pragma unroll
@@ -468,6 +483,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
           vz[0] &= k_lo, vz[1] &= k_hi;
         }
         mma_k16(oz, vz[0], 0u, vz[1], 0u, pb[y][0], pb[y][1]);
+        if constexpr (kFine) mma_k16(oz, vz[0], 0u, vz[1], 0u, pl[y][0], pl[y][1]);
         uint32_t va[4][NG / 2];          // entries 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -487,6 +503,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) int4_attend_kernel(At
           mma_k16(o[2 * g], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, q0, q1);
           mma_k16(o[2 * g + 1], (lo >> 8) & 0x000f000fu, (lo >> 8) & 0x00f000f0u, (hi >> 8) & 0x000f000fu,
                   (hi >> 8) & 0x00f000f0u, q0, q1);
+          if constexpr (kFine) {
+            const uint32_t r0 = hfma2(pl[y][0], vs[g][0], hfma2(pb[y][0], vs[g][0], q0 ^ 0x80008000u));
+            const uint32_t r1 = hfma2(pl[y][1], vs[g][1], hfma2(pb[y][1], vs[g][1], q1 ^ 0x80008000u));
+            mma_k16(o[2 * g], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, r0, r1);
+            mma_k16(o[2 * g + 1], (lo >> 8) & 0x000f000fu, (lo >> 8) & 0x00f000f0u, (hi >> 8) & 0x000f000fu,
+                    (hi >> 8) & 0x00f000f0u, r0, r1);
+          }
         }
       }
       {                                  // every lane has read the pages: their stage takes the next ones

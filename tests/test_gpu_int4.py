@@ -571,3 +571,26 @@ def test_scratch_is_asked_for_before_capture():
     g2.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, c.attend(q, accumulate=False))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp16_outputs_are_as_good_as_their_type(D):
+    """For fp16 no rounding of the weights shows beside the output's own: what is left of a weight and of its
+    product with a scale after two parts is 2^-21 of it (or 2^-24 / 16 where it is subnormal, times a code
+    or zero below 2^6), and n float32 additions lose n 2^-23. A small q keeps e_p small."""
+    lens = [2, 3, 5, 9, 33]
+    c, *_ = _filled(lens, 2, D, "fp16", seed=5)
+    q = _draw(83, (len(lens), 8, D), "fp16", 0.1)
+    out = _np(c.attend(q, accumulate=False))
+    qn = _np(q)
+    for u in range(c.units):
+        n, b, h = lens[u // 2], u // 2, u % 2
+        k, v, ka, vz, vcs = _exact_entries(c, u, n)
+        qq = qn[b, 4 * h:4 * h + 4]
+        o, p = P.int4_attend(qq, k, v)
+        S = (ka @ np.abs(qq).T / np.sqrt(D)).max(0)
+        ep = ((2 * D + 8) * S + 16) * 2.0 ** -24
+        A, Z = p.T @ vcs, p.T @ vz
+        tol = U["fp16"] * np.abs(o) + ((n + 4) * 2.0 ** -23 + 2 * ep[:, None]) * (A + Z) + n * 2.0 ** -22
+        err = np.abs(out[b, 4 * h:4 * h + 4] - o)
+        assert (err <= tol).all(), (u, n, float((err / tol).max()))
