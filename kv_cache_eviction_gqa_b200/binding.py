@@ -629,6 +629,8 @@ def _on(index: int, stream=None):
     """The context in which a call goes to a device and what it allocates belongs to its stream (nothing to
     do for the current device's current stream)."""
     if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
         return torch.cuda.stream(stream)
     return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
 

@@ -172,3 +172,11 @@ def test_int4_evict_refuses_more_newest_than_the_budget(L):
     """Which of the newest entries to drop is not defined."""
     c, d = _cache(), _cache(pages=2 * FAKE, lengths=2 * FAKE, seen=2 * FAKE, mass=2 * FAKE, pos=2 * FAKE)
     assert L.qe_int4_evict(C.byref(c), C.byref(d), 8, 9, None) == -1
+
+
+def test_a_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+
+    from kv_cache_eviction_gqa_b200 import binding
+    with pytest.raises(ValueError, match="cuda:1"):
+        binding._on(0, SimpleNamespace(device_index=1))
