@@ -493,9 +493,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         blocks0 += n0, blocks1 += n1;
         used0 += n0 > 0, used1 += n1 > 0;
       }
-      // the arrivals that the commits above announce land before the CTA leaves
+      // the arrivals that the commits above announce land before the CTA leaves, even if a wait gave up
       mma_commit_by(lead, drain);
-      wait(drain, 0, 5016);
+      mbar_wait_bounded(drain, 0, a.status, 5016);
     }
   } else {
     // ---- softmax ----
